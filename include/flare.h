@@ -536,6 +536,107 @@ FLARE_API flare_status_t flare_exp_split(int kernel, int64_t M, int64_t D, flare
 FLARE_API flare_status_t flare_eval_exp2(const float* x, float* y, int64_t n, int form,
                                          void* stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention over all pairs of queries and keys, and the per-head
+ * norms with position rotation that prepare its (or FLARE's) inputs.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Attention forward, per batch b, query head h and key head h / (Hq / Hk):
+ *   Y[i] = sum_j P[i][j] V[j],  P[i] = softmax over j of scale Q[i].K[j].
+ * Q, Y [B,Hq,Nq,D]; K, V [B,Hk,Nk,D]; Hq a multiple of Hk (the query heads
+ * of a key head are neighbours).  Float32 or bf16 throughout; sums and the
+ * softmax in float32.  With FLARE_BF16 the probabilities are rounded to bf16
+ * before their product with V (so are P and dS in the backward).
+ *
+ *   strides   NULL (contiguous) or 4 entries: Q, K, V, Y.  As for the *_ex
+ *             calls, except that Q, K and V may have a batch or head stride
+ *             of 0 (one batch or head shared by all), and that the stride of
+ *             a dimension of one entry is ignored.
+ *   q_lens,   NULL, or device int32 [B]: only the first q_lens[b] queries
+ *   k_lens    and k_lens[b] keys of batch b count.  Rows past them are never
+ *             used, whatever they hold; Y is 0 and lse -inf there.  A length
+ *             outside [0, Nq] or [0, Nk] is clamped and reported by
+ *             flare_device_status (FLARE_ERR_INVALID_ARG).
+ *   causal    nonzero: query i sees keys j <= i + (keys - queries), counted
+ *             with the lengths, so that the last query sees the last key.  A
+ *             query that sees no key has Y = 0 and lse = -inf.
+ *   lse_save  NULL, or float32 [B,Hq,Nq]: log of the softmax's denominator.
+ *   workspace flare_attn_workspace_size(0, ...) bytes, 256-byte aligned.
+ *
+ * Supported: D a multiple of 8 up to 128; Nq, Nk <= 2^30; B Hq <= 65535;
+ * scale finite and > 0.  K and V of a key that the mask hides from a query,
+ * but that lies within k_lens, have to be finite.  Results do not depend on
+ * timing (no atomics).  Enqueued on `stream`.
+ */
+FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void* Y,
+                                        const flare_strides_t* strides, const int32_t* q_lens,
+                                        const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk,
+                                        int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dtype,
+                                        float scale, int causal, float* lse_save, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Attention backward: dQ, dK, dV of sum(Y * dY) for the same arguments, with
+ * the probabilities recomputed from lse (flare_attn_fwd's lse_save) and Y:
+ *   dV = P^T dY,  dS = P (dY V^T - sum_d dY Y),  dQ = scale dS K,
+ *   dK = scale dS^T Q,
+ * dK and dV summed over the query heads of a key head.  dQ, or dK and dV
+ * together, may be NULL (not wanted).  Gradients of rows past the lengths are
+ * 0; dY and Y are not read there.  strides: NULL or 8 entries: Q, K, V, Y,
+ * dY, dQ, dK, dV.  workspace: flare_attn_workspace_size(1, ...) bytes.
+ */
+FLARE_API flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
+                                        const void* dY, const float* lse, void* dQ, void* dK,
+                                        void* dV, const flare_strides_t* strides,
+                                        const int32_t* q_lens, const int32_t* k_lens, int64_t B,
+                                        int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D,
+                                        flare_dtype_t dtype, float scale, int causal,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of flare_attn_fwd (backward = 0) or flare_attn_bwd (1) on
+ * the current device; 0 when the sizes are invalid or unsupported. */
+FLARE_API size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, int64_t Hk,
+                                           int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dtype);
+
+/*
+ * Norm of every query and key head and rotation by position, in one pass:
+ * per token and head, with weights w and the token's angles for the first R
+ * of the D elements,
+ *   u = w x / sqrt(mean(x^2) + eps),
+ *   (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin),   y = u past R,
+ * the pairs (a, b) being (i, i + R/2), or (2i, 2i + 1) when `interleaved`.
+ * q, qo [B,Hq,N,D]; k, ko [B,Hk,N,D]; wq, wk [D] in the same dtype, or NULL
+ * (ones); cos, sin float32 [N, R/2], or [B, N, R/2] with tab_batch_stride
+ * elements from one batch to the next (0: one table; a multiple of 4).
+ * Arithmetic in float32, one rounding at the end.  strides: NULL or 4
+ * entries: q, k, qo, ko (as flare_attn_fwd).  qo may be q, and ko k, with
+ * the same strides.  No workspace.
+ * Supported: D a multiple of 8 up to 128, R a multiple of 16 up to D (0: no
+ * rotation, cos and sin ignored), eps finite and > 0.
+ */
+FLARE_API flare_status_t flare_qk_norm_rope_fwd(
+    const void* q, const void* k, const void* wq, const void* wk, const float* cos,
+    const float* sin, int64_t tab_batch_stride, void* qo, void* ko, const flare_strides_t* strides,
+    int64_t B, int64_t Hq, int64_t Hk, int64_t N, int64_t D, int64_t R, int interleaved,
+    flare_dtype_t dtype, float eps, void* stream);
+
+/*
+ * Its gradient: dq, dk, and dwq, dwk [D] (each may be NULL: not wanted) from
+ * dqo, dko; the rows' scales are recomputed from q and k.  strides: NULL or 6
+ * entries: q, k, dqo, dko, dq, dk.  workspace:
+ * flare_qk_norm_rope_workspace_size bytes, 256-byte aligned.
+ */
+FLARE_API flare_status_t flare_qk_norm_rope_bwd(
+    const void* q, const void* k, const void* wq, const void* wk, const float* cos,
+    const float* sin, int64_t tab_batch_stride, const void* dqo, const void* dko, void* dq,
+    void* dk, void* dwq, void* dwk, const flare_strides_t* strides, int64_t B, int64_t Hq,
+    int64_t Hk, int64_t N, int64_t D, int64_t R, int interleaved, flare_dtype_t dtype, float eps,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+FLARE_API size_t flare_qk_norm_rope_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t N,
+                                                   int64_t D, flare_dtype_t dtype);
+
 /*
  * Launches one CTA that waits, with the kernels' bounded wait, on an
  * mbarrier that nothing arrives on, for limit_ns nanoseconds (at most the

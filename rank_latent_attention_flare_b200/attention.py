@@ -1,0 +1,330 @@
+"""Thin PyTorch binding of the attention calls: softmax attention over all
+pairs (``attn``) and the per-head norms with position rotation
+(``qk_norm_rope``), forward, backward and as autograd functions.
+
+Argument marshalling only, as in the FLARE binding: outputs and workspaces are
+allocated with torch on the tensors' device, for the stream the call runs on,
+and everything is computed in ``libflare.so``.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import functools
+import importlib
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from ._lib import FlareError
+
+_f = importlib.import_module(__package__ + ".flare")
+
+
+def _on(device: torch.device, stream):
+    """Makes the tensors' device, and ``stream`` when given, current: the
+    call's buffers then belong to the stream that uses them."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _same(what: str, *ts):
+    """Checks 4-D views with D contiguous, of one device and dtype."""
+    first = ts[0]
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError(f"{what} tensors must live on a CUDA device")
+        if t.dim() != 4 or t.stride(-1) != 1:
+            raise ValueError(f"{what} tensors must be [B,H,N,D] views with D contiguous")
+        if t.device != first.device or t.dtype != first.dtype:
+            raise ValueError(f"{what} tensors differ in device or dtype")
+
+
+def _shape(name: str, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _rows(name: str, t, shape, device):
+    if t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor on the tensors' device")
+    _shape(name, t, shape)
+
+
+def _workspace(workspace, nbytes: int, device, where: str):
+    if workspace is None:
+        if nbytes == 0:
+            raise FlareError(2, where)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
+    return workspace
+
+
+# ------------------------------------------------------------------ attention
+
+@functools.lru_cache(maxsize=1024)
+def _attn_bytes(backward: int, B, Hq, Hk, Nq, Nk, D, code: int, device: int) -> int:
+    return int(_lib.load().flare_attn_workspace_size(backward, B, Hq, Hk, Nq, Nk, D, code))
+
+
+def attn_workspace_size(backward: bool, B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int,
+                        dtype: torch.dtype) -> int:
+    """Workspace bytes of attn_fwd or attn_bwd on the current device (0:
+    unsupported sizes)."""
+    code = _lib.FLARE_F32 if dtype == torch.float32 else _lib.FLARE_BF16
+    return int(_lib.load().flare_attn_workspace_size(int(bool(backward)), B, Hq, Hk, Nq, Nk, D,
+                                                     code))
+
+
+def _attn_dims(q, k, v):
+    _same("attention", q, k, v)
+    B, Hq, Nq, D = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    _shape("k", k, (B, Hk, Nk, D))
+    _shape("v", v, (B, Hk, Nk, D))
+    if Hk == 0 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
+    return B, Hq, Hk, Nq, Nk, D
+
+
+def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
+             q_lens: Optional[torch.Tensor] = None, k_lens: Optional[torch.Tensor] = None,
+             save: bool = False, workspace: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, stream=None):
+    """Softmax attention softmax(scale q k^T) v.  Returns y, or (y, lse) when
+    ``save`` (lse float32 [B,Hq,Nq], for attn_bwd).
+
+    q [B,Hq,Nq,D]; k, v [B,Hk,Nk,D] with Hq a multiple of Hk (the query heads
+    of a key head are neighbours); D a multiple of 8 up to 128.  All may be
+    any views with D contiguous, k, v and q also expanded over batch or heads;
+    y takes q's layout.  ``q_lens``, ``k_lens`` (int32 [B] on the device):
+    valid queries and keys; rows past them are never used and y is 0 there.
+    ``causal``: query i sees keys j <= i + (keys - queries), counted with the
+    lengths.  A query that sees no key gives 0."""
+    B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
+    dev = q.device
+    code = _f._dtype_code(q)
+    s = _f.default_scale(D) if scale is None else float(scale)
+    ql, kl = _f._seq_lens(q_lens, B, dev), _f._seq_lens(k_lens, B, dev)
+    with _on(dev, stream):
+        y = torch.empty_like(q) if out is None else out
+        if out is not None:
+            _same("attention", q, out)
+            _shape("out", out, q.shape)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if save else None
+        ws = _workspace(workspace, _attn_bytes(0, B, Hq, Hk, Nq, Nk, D, code, dev.index), dev,
+                        "flare_attn_workspace_size")
+        st = _lib.load().flare_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _f._strides(q, k, v, y),
+            None if ql is None else ql.data_ptr(), None if kl is None else kl.data_ptr(),
+            B, Hq, Hk, Nq, Nk, D, code, s, int(bool(causal)),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+            torch.cuda.current_stream().cuda_stream)
+    _lib.check(st, "flare_attn_fwd")
+    return (y, lse) if save else y
+
+
+def attn_bwd(q, k, v, y, dy, lse, scale: Optional[float] = None, *, causal: bool = False,
+             q_lens: Optional[torch.Tensor] = None, k_lens: Optional[torch.Tensor] = None,
+             need_dq: bool = True, need_dkv: bool = True,
+             workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, dv) of attn_fwd for the upstream gradient dy, from
+    its output y and lse (``save=True``).  ``need_dq`` / ``need_dkv``: what is
+    not wanted is not computed and comes back as None."""
+    B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
+    _same("attention", q, y, dy)
+    _shape("y", y, q.shape)
+    _shape("dy", dy, q.shape)
+    dev = q.device
+    _rows("lse", lse, (B, Hq, Nq), dev)
+    if not (need_dq or need_dkv):
+        return None, None, None
+    code = _f._dtype_code(q)
+    s = _f.default_scale(D) if scale is None else float(scale)
+    ql, kl = _f._seq_lens(q_lens, B, dev), _f._seq_lens(k_lens, B, dev)
+    with _on(dev, stream):
+        dq = torch.empty_like(q) if need_dq else None
+        dk = torch.empty_like(k) if need_dkv else None
+        dv = torch.empty_like(v) if need_dkv else None
+        ws = _workspace(workspace, _attn_bytes(1, B, Hq, Hk, Nq, Nk, D, code, dev.index), dev,
+                        "flare_attn_workspace_size")
+        strides = _f._strides(q, k, v, y, dy, q if dq is None else dq, k if dk is None else dk,
+                              v if dv is None else dv)
+        st = _lib.load().flare_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), dy.data_ptr(), lse.data_ptr(),
+            None if dq is None else dq.data_ptr(), None if dk is None else dk.data_ptr(),
+            None if dv is None else dv.data_ptr(), strides,
+            None if ql is None else ql.data_ptr(), None if kl is None else kl.data_ptr(),
+            B, Hq, Hk, Nq, Nk, D, code, s, int(bool(causal)), ws.data_ptr(), ws.numel(),
+            torch.cuda.current_stream().cuda_stream)
+    _lib.check(st, "flare_attn_bwd")
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------- norms and rotation
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(B, Hq, Hk, N, D, code: int, device: int) -> int:
+    return int(_lib.load().flare_qk_norm_rope_workspace_size(B, Hq, Hk, N, D, code))
+
+
+def _norm_args(q, k, wq, wk, cos, sin):
+    """Sizes (B, Hq, Hk, N, D, R) and the table's batch stride."""
+    _same("query and key", q, k)
+    B, Hq, N, D = q.shape
+    _shape("k", k, (B, k.shape[1], N, D))
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is None:
+            continue
+        if w.dtype != q.dtype or w.device != q.device or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of the heads' device and dtype")
+        _shape(name, w, (D,))
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    R, sb = 0, 0
+    if cos is not None:
+        R = 2 * cos.shape[-1]
+        shape = (B, N, R // 2) if cos.dim() == 3 else (N, R // 2)
+        _rows("cos", cos, shape, q.device)
+        _rows("sin", sin, shape, q.device)
+        sb = N * (R // 2) if cos.dim() == 3 else 0
+        if R == 0:
+            raise ValueError("cos and sin are empty; leave them out for no rotation")
+    return B, Hq, k.shape[1], N, D, R, sb
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float = 1e-6,
+                     interleaved: bool = False, out=None, stream=None):
+    """Norm of every head of q [B,Hq,N,D] and k [B,Hk,N,D] and rotation by
+    position in one pass: u = w x / sqrt(mean(x^2) + eps), then the first R
+    elements of u turned in pairs by the token's angles.  Returns (qo, ko).
+
+    wq, wk: [D] weights in the heads' dtype (None: ones).  cos, sin: float32
+    [N, R/2], or [B, N, R/2] for positions of their own per batch element
+    (None: no rotation); R a multiple of 16 up to D, which is a multiple of 8
+    up to 128.  Pairs are (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
+    q and k may be any views with D contiguous; the outputs take their layout,
+    or go to ``out`` = (qo, ko), which may be q and k themselves."""
+    B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
+    code = _f._dtype_code(q)
+    with _on(q.device, stream):
+        if out is None:
+            qo, ko = torch.empty_like(q), torch.empty_like(k)
+        else:
+            qo, ko = out
+            _same("query and key", q, qo, ko)
+            _shape("out[0]", qo, q.shape)
+            _shape("out[1]", ko, k.shape)
+        st = _lib.load().flare_qk_norm_rope_fwd(
+            q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(cos), _p(sin), sb, qo.data_ptr(),
+            ko.data_ptr(), _f._strides(q, k, qo, ko), B, Hq, Hk, N, D, R, int(bool(interleaved)),
+            code, float(eps), torch.cuda.current_stream().cuda_stream)
+    _lib.check(st, "flare_qk_norm_rope_fwd")
+    return qo, ko
+
+
+def qk_norm_rope_bwd(q, k, wq, wk, cos, sin, dqo, dko, *, eps: float = 1e-6,
+                     interleaved: bool = False, need_dw: bool = True,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of qk_norm_rope_fwd; dwq, dwk are None
+    for weights that are None, or without ``need_dw``."""
+    B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
+    _same("query and key", q, dqo, dko)
+    _shape("dqo", dqo, q.shape)
+    _shape("dko", dko, k.shape)
+    code = _f._dtype_code(q)
+    dev = q.device
+    with _on(dev, stream):
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        dwq = torch.empty_like(wq) if need_dw and wq is not None else None
+        dwk = torch.empty_like(wk) if need_dw and wk is not None else None
+        ws = _workspace(workspace, _norm_bytes(B, Hq, Hk, N, D, code, dev.index), dev,
+                        "flare_qk_norm_rope_workspace_size")
+        st = _lib.load().flare_qk_norm_rope_bwd(
+            q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(cos), _p(sin), sb, dqo.data_ptr(),
+            dko.data_ptr(), dq.data_ptr(), dk.data_ptr(), _p(dwq), _p(dwk),
+            _f._strides(q, k, dqo, dko, dq, dk), B, Hq, Hk, N, D, R, int(bool(interleaved)), code,
+            float(eps), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    _lib.check(st, "flare_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+# -------------------------------------------------------------------- autograd
+
+def _grad_view(t: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient the library reads in place, else a contiguous copy."""
+    esz = t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        n == 1 or (s > 0 and (s * esz) % 16 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
+    return t if ok else t.contiguous()
+
+
+class AttnFunction(torch.autograd.Function):
+    """y = softmax attention (see attn_fwd); saves y and the row statistics,
+    the backward recomputes the probabilities."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens):
+        if not any(ctx.needs_input_grad):
+            return attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens)
+        y, lse = attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens, save=True)
+        ctx.save_for_backward(q, k, v, y, lse, q_lens, k_lens)
+        ctx.scale, ctx.causal = scale, causal
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, k, v, y, lse, q_lens, k_lens = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dq, dk, dv = attn_bwd(q, k, v, y, _grad_view(dy), lse, ctx.scale, causal=ctx.causal,
+                              q_lens=q_lens, k_lens=k_lens, need_dq=need[0],
+                              need_dkv=need[1] or need[2])
+        return dq, dk, dv, None, None, None, None
+
+
+class QkNormRopeFunction(torch.autograd.Function):
+    """(qo, ko) = norms and rotation (see qk_norm_rope_fwd)."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, cos, sin, eps, interleaved):
+        ctx.save_for_backward(q, k, wq, wk, cos, sin)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return qk_norm_rope_fwd(q, k, wq, wk, cos, sin, eps=eps, interleaved=interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dqo, dko):
+        q, k, wq, wk, cos, sin = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = qk_norm_rope_bwd(q, k, wq, wk, cos, sin, _grad_view(dqo), _grad_view(dko),
+                                 eps=ctx.eps, interleaved=ctx.interleaved,
+                                 need_dw=need[2] or need[3])
+        return (*grads, None, None, None, None)
+
+
+def attn(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
+         q_lens: Optional[torch.Tensor] = None,
+         k_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Softmax attention with autograd (arguments as attn_fwd)."""
+    return AttnFunction.apply(q, k, v, scale, causal, q_lens, k_lens)
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Per-head norms and position rotation with autograd (arguments as
+    qk_norm_rope_fwd); returns (qo, ko)."""
+    return QkNormRopeFunction.apply(q, k, wq, wk, cos, sin, eps, interleaved)

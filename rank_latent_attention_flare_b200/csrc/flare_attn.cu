@@ -1,0 +1,517 @@
+// Attention: cutting a call into CTAs, the workspace, the kernels common to
+// both paths (joining the forward's split records, the backward's per-query
+// statistics and partial sums), and the C entry points.
+#include "flare_attn.cuh"
+
+namespace flare {
+
+// ------------------------------------------------------------------ plans
+
+namespace {
+
+// The number of parts to cut each unit's `tiles` into on `slots` SMs:
+// minimises waves x (tiles per part + set-up of a CTA), plus the cost of
+// joining the parts when there is more than one; all in units of one tile.
+int choose_splits(int64_t units, int64_t tiles, int slots, double setup, double join) {
+  int best = 1;
+  double best_cost = 1e300;
+  const int64_t hi = imin64(tiles, imax64(1, 4LL * slots / imax64(units, 1)));
+  for (int64_t s = 1; s <= hi; ++s) {
+    const int64_t waves = (units * s + slots - 1) / slots;
+    const double cost =
+        (double)waves * ((double)((tiles + s - 1) / s) + setup) + (s > 1 ? join : 0.0);
+    if (cost < best_cost - 1e-9) {
+      best_cost = cost;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
+  const bool tc = attn_tc(dt);
+  const int64_t G = d.G(), tile = tc ? kAttnTile : 64;
+  AttnPlan p;
+  // the queries of several heads of a key head share a tile when that cuts
+  // the number of tiles: their keys and values are then read once
+  if (d.q.sh != 0 || d.Hq == 1)
+    for (int64_t g = 2; g <= G; ++g)
+      if (G % g == 0 && g * d.Nq <= tile) p.hpt = (int)g;
+  const int64_t rows = p.hpt > 1 ? p.hpt * d.Nq : d.Nq;
+  p.qt = tc && rows > kAttnTile ? 2 : 1;
+  p.rows = (int)(tile * p.qt);
+  p.qblocks = (rows + p.rows - 1) / p.rows;
+  p.units = d.B * (d.Hq / p.hpt) * p.qblocks;
+  const int64_t ktiles = (d.Nk + tile - 1) / tile;
+  p.splits = tc ? choose_splits(p.units, ktiles, sms, p.qt == 2 ? 2.0 : 4.0, p.qt == 2 ? 4.0 : 8.0)
+                : choose_splits(p.units, ktiles, 2 * sms, 1.0, 2.0);
+  return p;
+}
+
+AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
+  const bool tc = attn_tc(dt);
+  AttnBwdPlan p;
+  p.tile = tc ? kAttnTile : 64;
+  p.ktiles = (d.Nk + p.tile - 1) / p.tile;
+  p.qtiles = (d.Nq + p.tile - 1) / p.tile;
+  p.dkv_units = d.B * d.Hk * p.ktiles;
+  p.dq_units = d.B * d.Hq * p.qtiles;
+  p.dkv_splits = choose_splits(p.dkv_units, d.G() * p.qtiles, sms, 2.0, 4.0);
+  p.dq_splits = choose_splits(p.dq_units, p.ktiles, sms, 2.0, 4.0);
+  return p;
+}
+
+namespace {
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
+
+AttnWs attn_ws_fwd(const AttnDims& d, flare_dtype_t, const AttnPlan& p) {
+  AttnWs w;
+  w.part_ml = 256;
+  const size_t recs = p.splits > 1 ? (size_t)p.units * p.splits * p.rows : 0;
+  w.part_o = up256(w.part_ml + recs * 8);
+  w.total = up256(w.part_o + recs * attn_dp(d.D) * 4);
+  return w;
+}
+
+AttnWs attn_ws_bwd(const AttnDims& d, flare_dtype_t, const AttnBwdPlan& p) {
+  AttnWs w;
+  const size_t dp = attn_dp(d.D);
+  w.stats = 256;
+  w.dq_part = up256(w.stats + (size_t)d.B * d.Hq * d.Nq * 8);
+  const size_t nq = p.dq_splits > 1 ? (size_t)p.dq_units * p.dq_splits * p.tile * dp * 4 : 0;
+  w.dkv_part = up256(w.dq_part + nq);
+  const size_t nk = p.dkv_splits > 1 ? (size_t)p.dkv_units * p.dkv_splits * p.tile * dp * 8 : 0;
+  w.total = up256(w.dkv_part + nk);
+  return w;
+}
+
+// ---------------------------------------------------------- common kernels
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void put(T* p, float v);
+template <>
+__device__ __forceinline__ void put<float>(float* p, float v) { *p = v; }
+template <>
+__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* p, float v) {
+  *p = __float2bfloat16_rn(v);
+}
+
+// Joins the records (ref, sum, O) of the splits of one query row: weights
+// 2^(ref_s - max ref), added in split order (the result does not depend on
+// timing).  One warp per row, DP / 32 columns per lane.  Bound by latency:
+// the records were just written and sit in L2.
+template <typename T, int DP>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnFwdArgs A,
+                                                        int rows) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int E = DP / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (int64_t)A.B * A.Hq * A.Nq) return;
+  const int i = (int)(row % A.Nq);
+  const int64_t bh = row / A.Nq;
+  const int h = (int)(bh % A.Hq);
+  const int64_t b = bh / A.Hq;
+  // where the forward kernel put the row
+  int64_t unit;
+  int r;
+  if (A.hpt > 1) {
+    unit = b * (A.Hq / A.hpt) + h / A.hpt;
+    r = (h % A.hpt) * A.Nq + i;
+  } else {
+    unit = bh * A.qblocks + i / rows;
+    r = i % rows;
+  }
+  const int64_t rec0 = unit * A.splits * rows + r;   // + s * rows
+  float m = -INFINITY;
+  for (int s = lane; s < A.splits; s += 32) {
+    const float2 ml = A.part_ml[rec0 + (int64_t)s * rows];
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  float acc[E] = {};
+  float l = 0.f;
+  for (int s0 = 0; s0 < A.splits; s0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (s0 + lane < A.splits) ml = A.part_ml[rec0 + (int64_t)(s0 + lane) * rows];
+    const float wl = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+    const int cnt = min(32, A.splits - s0);
+    for (int s = 0; s < cnt; ++s) {
+      const float ls = __shfl_sync(0xffffffffu, ml.y, s);
+      const float w = __shfl_sync(0xffffffffu, wl, s);
+      if (ls == 0.f) continue;
+      l += w * ls;
+      const float* o = A.part_o + (rec0 + (int64_t)(s0 + s) * rows) * DP + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * o[e];
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  T* y = (T*)A.Y + b * A.y.sb + h * A.y.sh + i * A.y.sn + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (lane * E + e < A.D) put<T>(y + e, l != 0.f ? acc[e] * inv : 0.f);
+  if (A.lse && lane == 0) A.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Backward, before the products: per query row -lse in log2 units (-inf for
+// a row without weight, so that its P is exactly 0) and
+// delta = sum_d dY Y (= sum_j P dP, the softmax's Jacobian term).
+// LP lanes per row of 16-byte loads; bound by reading Y and dY once.
+template <typename T, int LP>
+__global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __grid_constant__ AttnBwdArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = 16 / sizeof(T);
+  if (blockIdx.x == 0 && threadIdx.x < 32)
+    attn_check_lens(A.q_lens, A.k_lens, A.B, A.Nq, A.Nk, A.err);
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LP;
+  const int sub = threadIdx.x % LP;
+  const bool in = row < (int64_t)A.B * A.Hq * A.Nq;
+  const int i = (int)(row % A.Nq);
+  const int64_t bh = row / A.Nq;
+  const int h = (int)(bh % A.Hq);
+  const int64_t b = bh / A.Hq;
+  bool live = in;
+  if (in && A.q_lens) live = i < A.q_lens[b];
+  float s = 0.f;
+  if (live && sub * V < A.D) {
+    const uint4 y = *reinterpret_cast<const uint4*>((const T*)A.Y + b * A.y.sb + h * A.y.sh +
+                                                    i * A.y.sn + sub * V);
+    const uint4 g = *reinterpret_cast<const uint4*>((const T*)A.dY + b * A.dy.sb + h * A.dy.sh +
+                                                    i * A.dy.sn + sub * V);
+    const uint32_t yy[4] = {y.x, y.y, y.z, y.w}, gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (sizeof(T) == 4) {
+        s += __uint_as_float(yy[k]) * __uint_as_float(gg[k]);
+      } else {
+        s += __uint_as_float(yy[k] << 16) * __uint_as_float(gg[k] << 16);
+        s += __uint_as_float(yy[k] & 0xffff0000u) * __uint_as_float(gg[k] & 0xffff0000u);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = LP / 2; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (in && sub == 0) {
+    const float lse = live ? A.lse[row] : -INFINITY;
+    A.nl[row] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    A.delta[row] = lse == -INFINITY ? 0.f : s;
+  }
+}
+
+// dQ (WHICH = 0) or dK and dV (1) as the sum of the splits' float32 partials
+// in split order, scaled and rounded once.  Four columns per thread; bound by
+// reading the partials, which sit in L2.  Rows past the lengths were written
+// as zeros by the kernels themselves.
+template <typename T, int DP, int WHICH>
+__global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const __grid_constant__ AttnBwdArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int C = DP / 4;
+  const int H = WHICH ? A.Hk : A.Hq, N = WHICH ? A.Nk : A.Nq;
+  const int tiles = WHICH ? A.ktiles : A.qtiles, splits = WHICH ? A.dkv_splits : A.dq_splits;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int col = (int)(id % C) * 4;
+  const int64_t row = id / C;
+  if (row >= (int64_t)A.B * H * N || col >= A.D) return;
+  const int n = (int)(row % N);
+  const int64_t bh = row / N;
+  const int h = (int)(bh % H);
+  const int64_t b = bh / H;
+  const int64_t unit = bh * tiles + n / A.tile;
+  const int r = n % A.tile;
+#pragma unroll
+  for (int k = 0; k <= WHICH; ++k) {
+    // partials [unit][split][dK, dV][row][DP]
+    const float* p = (WHICH ? A.dkv_part : A.dq_part) +
+                     ((unit * splits * (1 + WHICH) + k) * A.tile + r) * (int64_t)DP + col;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < splits; ++x) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)x * (1 + WHICH) * A.tile * DP);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const Tok& t = WHICH ? (k ? A.dv : A.dk) : A.dq;
+    T* out = (T*)(WHICH ? (k ? A.dV : A.dK) : A.dQ) + b * t.sb + h * t.sh + n * t.sn + col;
+    const float f = k ? 1.f : A.scale;
+    put<T>(out, s.x * f), put<T>(out + 1, s.y * f), put<T>(out + 2, s.z * f),
+        put<T>(out + 3, s.w * f);
+  }
+}
+
+template <typename T>
+cudaError_t join_t(const AttnPlan& p, const AttnFwdArgs& a, int dp, cudaStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)a.B * a.Hq * a.Nq + 3) / 4));
+  if (dp == 32) return launch_pdl(attn_join_kernel<T, 32>, grid, 128, 0, st, a, p.rows);
+  if (dp == 64) return launch_pdl(attn_join_kernel<T, 64>, grid, 128, 0, st, a, p.rows);
+  return launch_pdl(attn_join_kernel<T, 128>, grid, 128, 0, st, a, p.rows);
+}
+
+template <typename T>
+cudaError_t prep_t(const AttnBwdArgs& a, cudaStream_t st) {
+  const int lanes = (int)((a.D * sizeof(T) + 15) / 16);
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+#define FLARE_PREP(LP) \
+  launch_pdl(attn_bwd_prep_kernel<T, LP>, dim3((unsigned)((rows * LP + 255) / 256)), 256, 0, st, a)
+  if (lanes <= 4) return FLARE_PREP(4);
+  if (lanes <= 8) return FLARE_PREP(8);
+  if (lanes <= 16) return FLARE_PREP(16);
+  return FLARE_PREP(32);
+#undef FLARE_PREP
+}
+
+template <typename T, int WHICH>
+cudaError_t sum_t(const AttnBwdArgs& a, int dp, cudaStream_t st) {
+  const int64_t rows = WHICH ? (int64_t)a.B * a.Hk * a.Nk : (int64_t)a.B * a.Hq * a.Nq;
+  const dim3 grid((unsigned)((rows * (dp / 4) + 255) / 256));
+  if (dp == 32) return launch_pdl(attn_bwd_sum_kernel<T, 32, WHICH>, grid, 256, 0, st, a);
+  if (dp == 64) return launch_pdl(attn_bwd_sum_kernel<T, 64, WHICH>, grid, 256, 0, st, a);
+  return launch_pdl(attn_bwd_sum_kernel<T, 128, WHICH>, grid, 256, 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_join(const AttnPlan& p, const AttnFwdArgs& a, int dp, flare_dtype_t dt,
+                             cudaStream_t st) {
+  return dt == FLARE_BF16 ? join_t<__nv_bfloat16>(p, a, dp, st) : join_t<float>(p, a, dp, st);
+}
+
+cudaError_t launch_attn_bwd_prep(const AttnBwdArgs& a, flare_dtype_t dt, cudaStream_t st) {
+  return dt == FLARE_BF16 ? prep_t<__nv_bfloat16>(a, st) : prep_t<float>(a, st);
+}
+
+cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int dp, flare_dtype_t dt, int which,
+                                cudaStream_t st) {
+  if (dt == FLARE_BF16)
+    return which ? sum_t<__nv_bfloat16, 1>(a, dp, st) : sum_t<__nv_bfloat16, 0>(a, dp, st);
+  return which ? sum_t<float, 1>(a, dp, st) : sum_t<float, 0>(a, dp, st);
+}
+
+// ------------------------------------------------------------- validation
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 148;   // B200
+  }
+  return n;
+}
+
+namespace {
+
+flare_status_t sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D,
+                     flare_dtype_t dt) {
+  if (B < 1 || Hq < 1 || Hk < 1 || Nq < 1 || Nk < 1 || D < 1) return FLARE_ERR_INVALID_ARG;
+  if (dt != FLARE_F32 && dt != FLARE_BF16) return FLARE_ERR_INVALID_ARG;
+  if (B > (1LL << 20) || Hq > (1LL << 16) || Hk > (1LL << 16)) return FLARE_ERR_INVALID_ARG;
+  if (Hq % Hk != 0) return FLARE_ERR_INVALID_ARG;
+  if (D % 8 != 0 || D > 128) return FLARE_ERR_UNSUPPORTED;
+  // 32-bit token indices (with room for a tile before and after)
+  if (Nq > (1LL << 30) || Nk > (1LL << 30)) return FLARE_ERR_UNSUPPORTED;
+  if (B * Hq > 65535) return FLARE_ERR_UNSUPPORTED;
+  if ((double)B * Hq * Nq * D >= 1099511627776.0 || (double)B * Hk * Nk * D >= 1099511627776.0)
+    return FLARE_ERR_INVALID_ARG;   // 2^40
+  return FLARE_OK;
+}
+
+}  // namespace
+
+flare_status_t check_ptr(const void* p) {
+  return (p != nullptr && ((uintptr_t)p & 15u) == 0) ? FLARE_OK : FLARE_ERR_INVALID_ARG;
+}
+
+// The rows of an output do not overlap when, in order of stride, every
+// dimension with more than one entry steps over all the rows of the
+// dimensions inside it.
+flare_status_t check_tok(const flare_strides_t* st, int64_t B, int64_t H, int64_t N, int64_t D,
+                         flare_dtype_t dt, bool output, Tok* out) {
+  const int64_t esz = dt == FLARE_F32 ? 4 : 2;
+  int64_t s[3] = {H * N * D, N * D, D};
+  if (st) s[0] = st->b_stride, s[1] = st->h_stride, s[2] = st->n_stride;
+  int64_t e[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (e[i] == 1) {
+      s[i] = i < 2 ? 0 : 16 / esz;   // not used
+      continue;
+    }
+    const bool zero_ok = !output && i < 2;
+    if (s[i] < (zero_ok ? 0 : 1) || s[i] >= (1LL << 40) / esz) return FLARE_ERR_INVALID_ARG;
+    if ((s[i] * esz) % 16 != 0) return FLARE_ERR_UNSUPPORTED;
+  }
+  *out = Tok{s[0], s[1], s[2]};
+  if (!output) return FLARE_OK;
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] < s[i]) {
+        const int64_t ts = s[i], te = e[i];
+        s[i] = s[j], e[i] = e[j];
+        s[j] = ts, e[j] = te;
+      }
+  int64_t span = D;
+  for (int i = 0; i < 3; ++i) {
+    if (e[i] == 1) continue;
+    if (s[i] < span) return FLARE_ERR_INVALID_ARG;
+    span += s[i] * (e[i] - 1);
+  }
+  return FLARE_OK;
+}
+
+flare_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || ((uintptr_t)ws & 255u) != 0) return FLARE_ERR_WORKSPACE;
+  return bytes >= need ? FLARE_OK : FLARE_ERR_WORKSPACE;
+}
+
+namespace {
+
+flare_status_t lens(const int32_t* p) {
+  return ((uintptr_t)p & 3u) == 0 ? FLARE_OK : FLARE_ERR_INVALID_ARG;
+}
+
+AttnDims dims(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D, int causal) {
+  AttnDims d;
+  d.B = B, d.Hq = Hq, d.Hk = Hk, d.Nq = Nq, d.Nk = Nk, d.D = D;
+  d.causal = causal != 0;
+  return d;
+}
+
+// Zero strides (broadcast, or a dimension of one entry) -> one entry in the
+// tensor map, coordinate 0.
+int bcast_bits(const Tok& t, int k) { return (t.sb == 0 ? 1 << k : 0) | (t.sh == 0 ? 8 << k : 0); }
+
+}  // namespace
+}  // namespace flare
+
+using namespace flare;
+
+extern "C" {
+
+size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
+                                 int64_t Nk, int64_t D, flare_dtype_t dt) {
+  if (sizes(B, Hq, Hk, Nq, Nk, D, dt) != FLARE_OK) return 0;
+  AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, 0);
+  const int sms = sm_count();
+  if (backward) return attn_ws_bwd(d, dt, attn_bwd_plan(d, dt, sms)).total;
+  // the plan of a call depends on whether its queries are broadcast over the
+  // heads: room for either
+  d.q.sh = 1;
+  const size_t own = attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
+  d.q.sh = 0;
+  const size_t rep = attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
+  return own > rep ? own : rep;
+}
+
+flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void* Y,
+                              const flare_strides_t* strides, const int32_t* q_lens,
+                              const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
+                              int64_t Nk, int64_t D, flare_dtype_t dt, float scale, int causal,
+                              float* lse_save, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  FLARE_TRY(sizes(B, Hq, Hk, Nq, Nk, D, dt));
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FLARE_ERR_INVALID_ARG;
+  const void* must[4] = {Q, K, V, Y};
+  for (const void* p : must) FLARE_TRY(check_ptr(p));
+  if (lse_save) FLARE_TRY(check_ptr(lse_save));
+  FLARE_TRY(lens(q_lens));
+  FLARE_TRY(lens(k_lens));
+  AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, causal);
+  FLARE_TRY(check_tok(strides ? strides + 0 : nullptr, B, Hq, Nq, D, dt, false, &d.q));
+  FLARE_TRY(check_tok(strides ? strides + 1 : nullptr, B, Hk, Nk, D, dt, false, &d.k));
+  FLARE_TRY(check_tok(strides ? strides + 2 : nullptr, B, Hk, Nk, D, dt, false, &d.v));
+  FLARE_TRY(check_tok(strides ? strides + 3 : nullptr, B, Hq, Nq, D, dt, true, &d.y));
+  d.q_lens = q_lens;
+  d.k_lens = k_lens;
+  const AttnPlan p = attn_plan(d, dt, sm_count());
+  const AttnWs w = attn_ws_fwd(d, dt, p);
+  FLARE_TRY(check_workspace(workspace, workspace_bytes, w.total));
+  if (p.units * p.splits > 0x7fffffffLL || B * Hq * Nq > 0x7fffffffLL * 4)
+    return FLARE_ERR_UNSUPPORTED;   // grid.x
+  note_error("%s", "");
+  char* ws = (char*)workspace;
+  cudaStream_t st = (cudaStream_t)stream;
+  AttnFwdArgs a = {};
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.hpt = p.hpt, a.qblocks = (int)p.qblocks, a.splits = p.splits, a.causal = d.causal;
+  a.units = p.units;
+  a.c = scale * kLog2e;
+  a.q_lens = q_lens, a.k_lens = k_lens;
+  a.q = d.q, a.k = d.k, a.v = d.v, a.y = d.y;
+  a.Y = Y;
+  a.lse = lse_save;
+  a.part_ml = (float2*)(ws + w.part_ml);
+  a.part_o = (float*)(ws + w.part_o);
+  a.err = (uint32_t*)ws;
+  a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2);
+  FLARE_CUDA(launch_attn_fwd_simt(Q, K, V, d, p, a, dt, st));
+  if (p.splits > 1) FLARE_CUDA(launch_attn_join(p, a, attn_dp(D), dt, st));
+  return FLARE_OK;
+}
+
+flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
+                              const void* dY, const float* lse, void* dQ, void* dK, void* dV,
+                              const flare_strides_t* strides, const int32_t* q_lens,
+                              const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
+                              int64_t Nk, int64_t D, flare_dtype_t dt, float scale, int causal,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  FLARE_TRY(sizes(B, Hq, Hk, Nq, Nk, D, dt));
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FLARE_ERR_INVALID_ARG;
+  // dQ, or dK and dV together, may be left out
+  if ((dK == nullptr) != (dV == nullptr) || (dQ == nullptr && dK == nullptr))
+    return FLARE_ERR_INVALID_ARG;
+  const void* must[9] = {Q,   K, V, Y, dY, lse, dQ ? dQ : dK, dK ? dK : dQ, dV ? dV : dQ};
+  for (const void* p : must) FLARE_TRY(check_ptr(p));
+  FLARE_TRY(lens(q_lens));
+  FLARE_TRY(lens(k_lens));
+  AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, causal);
+  Tok* where[8] = {&d.q, &d.k, &d.v, &d.y, &d.dy, &d.dq, &d.dk, &d.dv};
+  for (int i = 0; i < 8; ++i) {
+    const bool keys = i == 1 || i == 2 || i == 6 || i == 7;
+    if ((i == 5 && !dQ) || (i > 5 && !dK)) continue;
+    FLARE_TRY(check_tok(strides ? strides + i : nullptr, B, keys ? Hk : Hq, keys ? Nk : Nq, D, dt, i >= 5,
+                 where[i]));
+  }
+  d.q_lens = q_lens;
+  d.k_lens = k_lens;
+  const AttnBwdPlan p = attn_bwd_plan(d, dt, sm_count());
+  const AttnWs w = attn_ws_bwd(d, dt, p);
+  FLARE_TRY(check_workspace(workspace, workspace_bytes, w.total));
+  const int64_t most = 0x7fffffffLL;
+  if (p.dkv_units * p.dkv_splits > most || p.dq_units * p.dq_splits > most ||
+      B * Hq * Nq > most * 8 || B * Hk * Nk > most * 8)
+    return FLARE_ERR_UNSUPPORTED;   // grid.x
+  note_error("%s", "");
+  char* ws = (char*)workspace;
+  cudaStream_t st = (cudaStream_t)stream;
+  AttnBwdArgs a = {};
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.tile = p.tile, a.ktiles = (int)p.ktiles, a.qtiles = (int)p.qtiles;
+  a.dkv_splits = p.dkv_splits, a.dq_splits = p.dq_splits, a.causal = d.causal;
+  a.dkv_units = p.dkv_units, a.dq_units = p.dq_units;
+  a.scale = scale, a.c = scale * kLog2e;
+  a.q_lens = q_lens, a.k_lens = k_lens;
+  a.q = d.q, a.k = d.k, a.v = d.v, a.y = d.y, a.dy = d.dy, a.dq = d.dq, a.dk = d.dk, a.dv = d.dv;
+  a.Q = Q, a.K = K, a.V = V, a.Y = Y, a.dY = dY, a.lse = lse;
+  a.dQ = dQ, a.dK = dK, a.dV = dV;
+  a.nl = (float*)(ws + w.stats);
+  a.delta = a.nl + B * Hq * Nq;
+  a.dq_part = (float*)(ws + w.dq_part);
+  a.dkv_part = (float*)(ws + w.dkv_part);
+  a.err = (uint32_t*)ws;
+  a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2) |
+            (d.dy.sb == 0 ? 64 : 0) | (d.dy.sh == 0 ? 128 : 0);
+  FLARE_CUDA(launch_attn_bwd_prep(a, dt, st));
+  FLARE_CUDA(launch_attn_bwd_simt(d, p, a, dt, st));
+  if (dK && p.dkv_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 1, st));
+  if (dQ && p.dq_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 0, st));
+  return FLARE_OK;
+}
+
+}  // extern "C"

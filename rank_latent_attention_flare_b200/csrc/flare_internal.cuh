@@ -37,6 +37,15 @@ enum ErrorSite : uint32_t {
   kErrBwdBMmaWait = 0x502,
   kErrBwdBRowWait = 0x503,
   kErrSeqLen = 0x601,   // a sequence length outside [0, N] (clamped)
+  kErrAttnFwdTmaWait = 0x801,
+  kErrAttnFwdMmaWait = 0x802,
+  kErrAttnFwdRowWait = 0x803,
+  kErrAttnDkvTmaWait = 0x811,
+  kErrAttnDkvMmaWait = 0x812,
+  kErrAttnDkvRowWait = 0x813,
+  kErrAttnDqTmaWait = 0x821,
+  kErrAttnDqMmaWait = 0x822,
+  kErrAttnDqRowWait = 0x823,
 };
 
 // ------------------------------------------------------------------ planning
