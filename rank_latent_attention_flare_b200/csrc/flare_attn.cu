@@ -51,7 +51,7 @@ AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
 }
 
 AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
-  const bool tc = attn_tc(dt);
+  const bool tc = false;
   AttnBwdPlan p;
   p.tile = tc ? kAttnTile : 64;
   p.ktiles = (d.Nk + p.tile - 1) / p.tile;
@@ -450,7 +450,8 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   a.part_o = (float*)(ws + w.part_o);
   a.err = (uint32_t*)ws;
   a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2);
-  FLARE_CUDA(launch_attn_fwd_simt(Q, K, V, d, p, a, dt, st));
+  FLARE_CUDA(attn_tc(dt) ? launch_attn_fwd_tc(Q, K, V, d, p, a, st)
+                         : launch_attn_fwd_simt(Q, K, V, d, p, a, st));
   if (p.splits > 1) FLARE_CUDA(launch_attn_join(p, a, attn_dp(D), dt, st));
   return FLARE_OK;
 }

@@ -54,9 +54,14 @@ __device__ __forceinline__ int tile_row0(int t, int T, int n) { return min(t * T
 constexpr int kAttnTile = 128;   // query and key rows per tensor-core tile
 
 // Head dimension of the kernels: D is padded with the TMA's zero fill.
-inline int attn_dp(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int attn_dp(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 
-inline bool attn_tc(flare_dtype_t) { return false; }
+// 16-element steps of the tensor cores' products over D, a compile-time
+// constant of their kernels: the next of 2, 4, 5, 6, 8 (D = 80 and 96 are
+// common; the zero fill makes a larger step count exact for the rest).
+inline int attn_ks(int64_t D) { return D <= 32 ? 2 : D <= 64 ? 4 : D <= 80 ? 5 : D <= 96 ? 6 : 8; }
+
+inline bool attn_tc(flare_dtype_t dt) { return dt == FLARE_BF16; }
 
 // How the forward is cut.  A CTA takes `qt` tiles of query rows (tensor
 // cores: 128 rows each; CUDA cores: one tile of 64) of one head, or, when
@@ -134,9 +139,10 @@ struct AttnBwdArgs {
   int bcast;               // as AttnFwdArgs, with dy: bits 6 (batch) and 7 (head)
 };
 
+cudaError_t launch_attn_fwd_tc(const void* Q, const void* K, const void* V, const AttnDims& d,
+                               const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st);
 cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnDims& d,
-                                 const AttnPlan& p, const AttnFwdArgs& a, flare_dtype_t dt,
-                                 cudaStream_t st);
+                                 const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st);
 // Joins the records of the splits into Y and lse.
 cudaError_t launch_attn_join(const AttnPlan& p, const AttnFwdArgs& a, int dp, flare_dtype_t dt,
                              cudaStream_t st);

@@ -493,10 +493,8 @@ cudaError_t bwd_d(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
 }  // namespace
 
 cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnDims& d,
-                                 const AttnPlan& p, const AttnFwdArgs& a, flare_dtype_t dt,
-                                 cudaStream_t st) {
-  return dt == FLARE_BF16 ? fwd_d<__nv_bfloat16>(Q, K, V, d, p, a, st)
-                          : fwd_d<float>(Q, K, V, d, p, a, st);
+                                 const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st) {
+  return fwd_d<float>(Q, K, V, d, p, a, st);
 }
 
 cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
