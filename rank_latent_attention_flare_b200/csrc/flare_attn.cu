@@ -51,7 +51,7 @@ AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
 }
 
 AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
-  const bool tc = false;
+  const bool tc = attn_tc(dt);
   AttnBwdPlan p;
   p.tile = tc ? kAttnTile : 64;
   p.ktiles = (d.Nk + p.tile - 1) / p.tile;
@@ -209,8 +209,7 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __grid_constan
 
 // dQ (WHICH = 0) or dK and dV (1) as the sum of the splits' float32 partials
 // in split order, scaled and rounded once.  Four columns per thread; bound by
-// reading the partials, which sit in L2.  Rows past the lengths were written
-// as zeros by the kernels themselves.
+// reading the partials, which sit in L2.  Rows past the lengths become zeros.
 template <typename T, int DP, int WHICH>
 __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const __grid_constant__ AttnBwdArgs A) {
   pdl_wait();
@@ -226,6 +225,8 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const __grid_constant
   const int64_t bh = row / N;
   const int h = (int)(bh % H);
   const int64_t b = bh / H;
+  const int32_t* lens = WHICH ? A.k_lens : A.q_lens;
+  const bool own = lens == nullptr || n < lens[b];
   const int64_t unit = bh * tiles + n / A.tile;
   const int r = n % A.tile;
 #pragma unroll
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const __grid_constant
     const float* p = (WHICH ? A.dkv_part : A.dq_part) +
                      ((unit * splits * (1 + WHICH) + k) * A.tile + r) * (int64_t)DP + col;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = 0; x < splits; ++x) {
+    for (int x = 0; own && x < splits; ++x) {
       const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)x * (1 + WHICH) * A.tile * DP);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
@@ -509,7 +510,7 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2) |
             (d.dy.sb == 0 ? 64 : 0) | (d.dy.sh == 0 ? 128 : 0);
   FLARE_CUDA(launch_attn_bwd_prep(a, dt, st));
-  FLARE_CUDA(launch_attn_bwd_simt(d, p, a, dt, st));
+  FLARE_CUDA(attn_tc(dt) ? launch_attn_bwd_tc(d, p, a, st) : launch_attn_bwd_simt(d, p, a, st));
   if (dK && p.dkv_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 1, st));
   if (dQ && p.dq_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 0, st));
   return FLARE_OK;

@@ -149,8 +149,10 @@ cudaError_t launch_attn_join(const AttnPlan& p, const AttnFwdArgs& a, int dp, fl
 // Per query: -lse in log2 units and delta = sum(dY * Y).
 cudaError_t launch_attn_bwd_prep(const AttnBwdArgs& a, flare_dtype_t dt, cudaStream_t st);
 // The products; dQ, or dK and dV, may be NULL (not wanted).
+cudaError_t launch_attn_bwd_tc(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
+                               cudaStream_t st);
 cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
-                                 flare_dtype_t dt, cudaStream_t st);
+                                 cudaStream_t st);
 // Sums the partials of the splits, in order, into dQ (which = 0) or dK and dV (1).
 cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int dp, flare_dtype_t dt, int which,
                                 cudaStream_t st);

@@ -18,42 +18,18 @@ constexpr int kT = 64;             // queries and keys per tile
 constexpr int kNT = 256;
 constexpr int kPS = kT + 4;        // row pitch of a 64 x 64 tile
 
-template <typename T>
-__device__ __forceinline__ void store_row(T* p, float v);
-template <>
-__device__ __forceinline__ void store_row<float>(float* p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void store_row<__nv_bfloat16>(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
-}
-
 // Rows [row0, row0 + 64) of p, the first n valid rows and D columns of it;
 // zeros elsewhere.
-template <typename T, int DP>
-__device__ __forceinline__ void load_rows(float* dst, const T* p, int64_t sn, int row0, int n,
+template <int DP>
+__device__ __forceinline__ void load_rows(float* dst, const float* p, int64_t sn, int row0, int n,
                                           int D) {
-  constexpr int V = 16 / sizeof(T), C = DP / V;
+  constexpr int C = DP / 4;
 #pragma unroll
   for (int x = threadIdx.x; x < kT * C; x += kNT) {
-    const int r = x / C, c = (x % C) * V;
-    float f[V] = {};
-    if (row0 + r < n && c < D) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p + (row0 + r) * sn + c);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 4) {
-          f[k] = __uint_as_float(w[k]);
-        } else {
-          f[2 * k] = __uint_as_float(w[k] << 16);
-          f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < V; k += 4)
-      *reinterpret_cast<float4*>(dst + r * (DP + 4) + c + k) =
-          make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    const int r = x / C, c = (x % C) * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + r < n && c < D) f = *reinterpret_cast<const float4*>(p + (row0 + r) * sn + c);
+    *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = f;
   }
 }
 
@@ -126,8 +102,8 @@ __device__ __forceinline__ void prod_nn(const float* P, const float* B, int ty, 
 }
 
 // Writes a thread's 4 rows times f as rows [row0, n) of a token tensor.
-template <typename T, int DP>
-__device__ __forceinline__ void put_rows(T* p, int64_t sn, int row0, int n, int D, int ty, int tx,
+template <int DP>
+__device__ __forceinline__ void put_rows(float* p, int64_t sn, int row0, int n, int D, int ty, int tx,
                                          const float (&c)[4][DP / 16], const float (&f)[4]) {
   using C = Cols<DP>;
 #pragma unroll
@@ -139,7 +115,7 @@ __device__ __forceinline__ void put_rows(T* p, int64_t sn, int row0, int n, int 
 #pragma unroll
       for (int w = 0; w < C::W; ++w) {
         const int col = C::at(tx, g) + w;
-        if (col < D) store_row<T>(p + r * sn + col, c[i][g * C::W + w] * f[i]);
+        if (col < D) p[r * sn + col] = c[i][g * C::W + w] * f[i];
       }
   }
 }
@@ -173,9 +149,9 @@ constexpr int kPFloats = kT * kPS;
 // Forward: one CTA = 64 query rows (of one head, or of hpt heads that share
 // a key head) and one part of the key tiles.  The running maximum and sum of
 // a row are held by the 16 threads that share it.  P overwrites the key tile.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kNT)
-    attn_fwd_simt_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
+    attn_fwd_simt_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
                          const __grid_constant__ AttnFwdArgs A) {
   pdl_wait();
   pdl_trigger();
@@ -212,18 +188,18 @@ __global__ void __launch_bounds__(kNT)
   }
   if (packed) {
     for (int g = 0; g < A.hpt; ++g) {   // one head's queries at a time
-      const T* p = Q + b * A.q.sb + (h0 + g) * A.q.sh;
+      const float* p = Q + b * A.q.sb + (h0 + g) * A.q.sh;
       for (int x = threadIdx.x; x < A.Nq * DP; x += kNT) {
         const int i = x / DP, d = x % DP;
         float f = 0.f;
-        if (i < sq.ql && d < A.D) f = to_f(p[i * A.q.sn + d]);
+        if (i < sq.ql && d < A.D) f = p[i * A.q.sn + d];
         qs[(g * A.Nq + i) * (DP + 4) + d] = f;
       }
     }
     for (int x = threadIdx.x + A.hpt * A.Nq * DP; x < kT * DP; x += kNT)
       qs[x / DP * (DP + 4) + x % DP] = 0.f;
   } else {
-    load_rows<T, DP>(qs, Q + b * A.q.sb + h0 * A.q.sh, A.q.sn, q0, sq.ql, A.D);
+    load_rows<DP>(qs, Q + b * A.q.sb + h0 * A.q.sh, A.q.sn, q0, sq.ql, A.D);
   }
 
   float m[4], l[4], o[4][DP / 16];
@@ -233,12 +209,12 @@ __global__ void __launch_bounds__(kNT)
 #pragma unroll
     for (int e = 0; e < DP / 16; ++e) o[i][e] = 0.f;
   }
-  const T* kp = K + b * A.k.sb + hk * A.k.sh;
-  const T* vp = V + b * A.v.sb + hk * A.v.sh;
+  const float* kp = K + b * A.k.sb + hk * A.k.sh;
+  const float* vp = V + b * A.v.sb + hk * A.v.sh;
   for (int t = lo; t < hi; ++t) {
     __syncthreads();
-    load_rows<T, DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
-    load_rows<T, DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
+    load_rows<DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
+    load_rows<DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
     __syncthreads();
     float s[4][4];
     prod_nt<DP>(qs, ks, ty, tx, s);
@@ -287,11 +263,11 @@ __global__ void __launch_bounds__(kNT)
   for (int i = 0; i < 4; ++i) {
     if (!live[i]) continue;
     const bool some = qi[i] < sq.ql && l[i] != 0.f;
-    T* y = (T*)A.Y + b * A.y.sb + qh[i] * A.y.sh + qi[i] * A.y.sn;
+    float* y = (float*)A.Y + b * A.y.sb + qh[i] * A.y.sh + qi[i] * A.y.sn;
 #pragma unroll
     for (int e = 0; e < DP / 16; ++e) {
       const int col = Cols<DP>::at(tx, e / Cols<DP>::W) + e % Cols<DP>::W;
-      if (col < A.D) store_row<T>(y + col, some ? o[i][e] / l[i] : 0.f);
+      if (col < A.D) y[col] = some ? o[i][e] / l[i] : 0.f;
     }
     if (A.lse && tx == 0)
       A.lse[((int64_t)b * A.Hq + qh[i]) * A.Nq + qi[i]] =
@@ -302,7 +278,7 @@ __global__ void __launch_bounds__(kNT)
 // dK and dV of 64 keys: over the query tiles of the heads that share them,
 //   P^T = 2^(c K Q^T + nl),  dV += P^T dY,
 //   dS^T = P^T (V dY^T - delta),  dK += dS^T Q.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constant__ AttnBwdArgs A) {
   pdl_wait();
   pdl_trigger();
@@ -326,14 +302,14 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
   const int per = k0 < sq.kl ? max(0, (sq.ql + kT - 1) / kT - first) : 0;   // tiles of a head
   const int lo = (int)((int64_t)per * G * split / A.dkv_splits);
   const int hi = (int)((int64_t)per * G * (split + 1) / A.dkv_splits);
-  load_rows<T, DP>(ks, (const T*)A.K + b * A.k.sb + hk * A.k.sh, A.k.sn, k0, sq.kl, A.D);
-  load_rows<T, DP>(vs, (const T*)A.V + b * A.v.sb + hk * A.v.sh, A.v.sn, k0, sq.kl, A.D);
+  load_rows<DP>(ks, (const float*)A.K + b * A.k.sb + hk * A.k.sh, A.k.sn, k0, sq.kl, A.D);
+  load_rows<DP>(vs, (const float*)A.V + b * A.v.sb + hk * A.v.sh, A.v.sn, k0, sq.kl, A.D);
   float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
   for (int it = lo; it < hi; ++it) {
     const int h = hk * G + it / per, q0 = (first + it % per) * kT;
     __syncthreads();
-    load_rows<T, DP>(qs, (const T*)A.Q + b * A.q.sb + h * A.q.sh, A.q.sn, q0, sq.ql, A.D);
-    load_rows<T, DP>(gs, (const T*)A.dY + b * A.dy.sb + h * A.dy.sh, A.dy.sn, q0, sq.ql, A.D);
+    load_rows<DP>(qs, (const float*)A.Q + b * A.q.sb + h * A.q.sh, A.q.sn, q0, sq.ql, A.D);
+    load_rows<DP>(gs, (const float*)A.dY + b * A.dy.sb + h * A.dy.sh, A.dy.sn, q0, sq.ql, A.D);
     if (threadIdx.x < kT) {
       const int64_t row = ((int64_t)b * A.Hq + h) * A.Nq + q0 + threadIdx.x;
       const bool in = q0 + threadIdx.x < sq.ql;
@@ -374,12 +350,12 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
     return;
   }
   const float fs[4] = {A.scale, A.scale, A.scale, A.scale}, f1[4] = {1.f, 1.f, 1.f, 1.f};
-  put_rows<T, DP>((T*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk, fs);
-  put_rows<T, DP>((T*)A.dV + b * A.dv.sb + hk * A.dv.sh, A.dv.sn, k0, A.Nk, A.D, ty, tx, dv, f1);
+  put_rows<DP>((float*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk, fs);
+  put_rows<DP>((float*)A.dV + b * A.dv.sb + hk * A.dv.sh, A.dv.sn, k0, A.Nk, A.D, ty, tx, dv, f1);
 }
 
 // dQ of 64 queries: over the key tiles they see, dQ += (P (dY V^T - delta)) K.
-template <typename T, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant__ AttnBwdArgs A) {
   pdl_wait();
   pdl_trigger();
@@ -400,8 +376,8 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
   const int nall = q0 < sq.ql ? sq.key_tiles(q0 + kT - 1, kT) : 0;
   const int lo = (int)((int64_t)nall * split / A.dq_splits);
   const int hi = (int)((int64_t)nall * (split + 1) / A.dq_splits);
-  load_rows<T, DP>(qs, (const T*)A.Q + b * A.q.sb + h * A.q.sh, A.q.sn, q0, sq.ql, A.D);
-  load_rows<T, DP>(gs, (const T*)A.dY + b * A.dy.sb + h * A.dy.sh, A.dy.sn, q0, sq.ql, A.D);
+  load_rows<DP>(qs, (const float*)A.Q + b * A.q.sb + h * A.q.sh, A.q.sn, q0, sq.ql, A.D);
+  load_rows<DP>(gs, (const float*)A.dY + b * A.dy.sb + h * A.dy.sh, A.dy.sn, q0, sq.ql, A.D);
   float nl[4], dl[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -411,12 +387,12 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
     dl[i] = q < sq.ql ? A.delta[row] : 0.f;
   }
   float dq[4][DP / 16] = {};
-  const T* kp = (const T*)A.K + b * A.k.sb + hk * A.k.sh;
-  const T* vp = (const T*)A.V + b * A.v.sb + hk * A.v.sh;
+  const float* kp = (const float*)A.K + b * A.k.sb + hk * A.k.sh;
+  const float* vp = (const float*)A.V + b * A.v.sb + hk * A.v.sh;
   for (int t = lo; t < hi; ++t) {
     __syncthreads();
-    load_rows<T, DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
-    load_rows<T, DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
+    load_rows<DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
+    load_rows<DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
     __syncthreads();
     float s[4][4], dp[4][4];
     prod_nt<DP>(qs, ks, ty, tx, s);
@@ -442,7 +418,7 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
     return;
   }
   const float fs[4] = {A.scale, A.scale, A.scale, A.scale};
-  put_rows<T, DP>((T*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq, fs);
+  put_rows<DP>((float*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq, fs);
 }
 
 template <typename... KA, typename... As>
@@ -453,53 +429,42 @@ cudaError_t go(void (*kernel)(KA...), int64_t grid, int smem, cudaStream_t st, A
   return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
-template <typename T, int DP>
+template <int DP>
 cudaError_t fwd_t(const void* Q, const void* K, const void* V, const AttnPlan& p,
                   const AttnFwdArgs& a, cudaStream_t st) {
   const int last = tile_floats<DP>() > kPFloats ? tile_floats<DP>() : kPFloats;
-  return go(attn_fwd_simt_kernel<T, DP>, p.units * p.splits, (2 * tile_floats<DP>() + last) * 4, st,
-            (const T*)Q, (const T*)K, (const T*)V, a);
+  return go(attn_fwd_simt_kernel<DP>, p.units * p.splits, (2 * tile_floats<DP>() + last) * 4, st,
+            (const float*)Q, (const float*)K, (const float*)V, a);
 }
 
-template <typename T, int DP>
+template <int DP>
 cudaError_t bwd_t(const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
   const int smem = (4 * tile_floats<DP>() + kPFloats + 2 * kT) * 4;
   cudaError_t e = cudaSuccess;
-  if (a.dK) e = go(attn_dkv_simt_kernel<T, DP>, p.dkv_units * p.dkv_splits, smem, st, a);
+  if (a.dK) e = go(attn_dkv_simt_kernel<DP>, p.dkv_units * p.dkv_splits, smem, st, a);
   if (e == cudaSuccess && a.dQ)
-    e = go(attn_dq_simt_kernel<T, DP>, p.dq_units * p.dq_splits, smem, st, a);
+    e = go(attn_dq_simt_kernel<DP>, p.dq_units * p.dq_splits, smem, st, a);
   return e;
-}
-
-template <typename T>
-cudaError_t fwd_d(const void* Q, const void* K, const void* V, const AttnDims& d, const AttnPlan& p,
-                  const AttnFwdArgs& a, cudaStream_t st) {
-  switch (attn_dp(d.D)) {
-    case 32: return fwd_t<T, 32>(Q, K, V, p, a, st);
-    case 64: return fwd_t<T, 64>(Q, K, V, p, a, st);
-    default: return fwd_t<T, 128>(Q, K, V, p, a, st);
-  }
-}
-
-template <typename T>
-cudaError_t bwd_d(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
-  switch (attn_dp(d.D)) {
-    case 32: return bwd_t<T, 32>(p, a, st);
-    case 64: return bwd_t<T, 64>(p, a, st);
-    default: return bwd_t<T, 128>(p, a, st);
-  }
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnDims& d,
                                  const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st) {
-  return fwd_d<float>(Q, K, V, d, p, a, st);
+  switch (attn_dp(d.D)) {
+    case 32: return fwd_t<32>(Q, K, V, p, a, st);
+    case 64: return fwd_t<64>(Q, K, V, p, a, st);
+    default: return fwd_t<128>(Q, K, V, p, a, st);
+  }
 }
 
 cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
-                                 flare_dtype_t dt, cudaStream_t st) {
-  return dt == FLARE_BF16 ? bwd_d<__nv_bfloat16>(d, p, a, st) : bwd_d<float>(d, p, a, st);
+                                 cudaStream_t st) {
+  switch (attn_dp(d.D)) {
+    case 32: return bwd_t<32>(p, a, st);
+    case 64: return bwd_t<64>(p, a, st);
+    default: return bwd_t<128>(p, a, st);
+  }
 }
 
 }  // namespace flare

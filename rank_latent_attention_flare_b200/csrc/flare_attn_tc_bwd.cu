@@ -1,0 +1,720 @@
+// Tensor-core backward of softmax attention for sm_100a (bf16, D up to 128):
+// two kernels that recompute the probabilities, one over key tiles (dK, dV),
+// one over query tiles (dQ).  Each sum stays in one CTA's TMEM, so nothing is
+// added by atomics and results repeat bit by bit; the price is computing the
+// logits and dP twice, 7 products per tile pair instead of 5.
+//
+// dK, dV (attn_dkv_kernel): TMEM lanes are keys, columns queries.  Per tile
+// of 128 queries of each head that shares the keys:
+//   S^T = K Q^T,  P^T = 2^(c S^T + nl),   dV += P^T dY     (P^T from TMEM)
+//   dP^T = V dY^T, dS^T = P^T (dP^T - delta), dK += dS^T Q
+// nl = -lse and delta differ by column: they come from shared memory.
+// Warpgroup w computes columns [64 w, 64 w + 64).  P^T and dS^T (bf16)
+// replace the columns of S^T and dP^T that the same warp has read.  The
+// MMAs alternate with the softmax so that the tensor core always has two
+// products to run: {dV_j, S_j+1} while dS_j is computed, {dK_j, dP_j+1}
+// while P_j+1 is.
+//
+// dQ (attn_dq_kernel): lanes are queries, columns keys, nl and delta one per
+// lane:  S = Q K^T, dP = dY V^T, dS = P (dP - delta), dQ += dS K.  S has two
+// buffers, so that P_j+1 is computed while {dQ_j, dP_j+1} run.
+//
+// Every batch of MMAs has a compile-time length (KS steps over D), see the
+// forward.  The tensor core runs the MMAs of the issuing thread in order, so
+// S_j+1 may be issued behind the product that reads P_j from its columns.
+//
+// P in float32 enters dS; P and dS are rounded to bf16 for their products.
+// Bound: per tile pair 4 D clocks for each product against 1024 clocks for
+// the exponentials (a part of them on the FMA pipe): the tensor core for
+// D = 128, the softmax warps for D <= 64.
+#include "flare_attn_tc.cuh"
+
+namespace flare {
+namespace attn {
+namespace {
+
+// Every k-th pair of exponentials on the FMA pipe (tiles without a mask).
+constexpr int kBwdPoly = 3;
+
+// 2^(c a + n) for 64 values, in place, n[] per value (column) or one for all:
+// probabilities in float32.
+template <bool COLS, int POLY>
+__device__ __forceinline__ void exp64(uint32_t (&a)[64], float c, float n, const float* cols) {
+  const uint64_t c2 = f32x2(c, c);
+#pragma unroll
+  for (int t = 0; t < 64; t += 4) {
+    float4 v;
+    if (COLS) v = *reinterpret_cast<const float4*>(cols + t);
+    else v = make_float4(n, n, n, n);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = t + 2 * h;
+      const uint64_t x = fma_f32x2(f32x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), c2,
+                                   h ? f32x2(v.z, v.w) : f32x2(v.x, v.y));
+      float p0, p1;
+      if (POLY > 0 && (i / 2) % (POLY > 0 ? POLY : 1) == POLY - 1) {
+        exp2_fma_pair(x, p0, p1);
+      } else {
+        split_f32x2(x, p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+      }
+      a[i] = __float_as_uint(p0);
+      a[i + 1] = __float_as_uint(p1);
+    }
+  }
+}
+
+// 32 packed bf16 pairs of 64 values to TMEM.
+__device__ __forceinline__ void store_bf16_tmem(uint32_t taddr, const uint32_t (&a)[64]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      pk[t] = pack_bf16(__uint_as_float(a[32 * h + 2 * t]), __uint_as_float(a[32 * h + 2 * t + 1]));
+    tmem_st16(taddr + 16 * h, pk);
+  }
+}
+
+// dS = P (dP - delta), in place in g (dP on entry).
+template <bool COLS>
+__device__ __forceinline__ void ds64(uint32_t (&g)[64], const uint32_t (&p)[64], float d,
+                                     const float* cols) {
+#pragma unroll
+  for (int t = 0; t < 64; t += 4) {
+    float4 v;
+    if (COLS) v = *reinterpret_cast<const float4*>(cols + t);
+    else v = make_float4(d, d, d, d);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = t + 2 * h;
+      const uint64_t x =
+          mul_f32x2(f32x2(__uint_as_float(p[i]), __uint_as_float(p[i + 1])),
+                    sub_f32x2(f32x2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])),
+                              h ? f32x2(v.z, v.w) : f32x2(v.x, v.y)));
+      float x0, x1;
+      split_f32x2(x, x0, x1);
+      g[i] = __float_as_uint(x0);
+      g[i + 1] = __float_as_uint(x1);
+    }
+  }
+}
+
+// TMEM column of K step kk (16 rows) of a bf16 operand stored by two
+// warpgroups, each in the first half of its own 64 columns.
+__device__ __forceinline__ constexpr uint32_t a_step(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }
+
+// One lane's row of an accumulator of DP columns: as bf16 times f to `out`
+// (columns below D), or as float32 to a record, or zeros.  Whole-warp call.
+template <int DP>
+__device__ __forceinline__ void put_row(uint32_t taddr, bool have, bool some, float f,
+                                        __nv_bfloat16* out, float* rec, bool live, int D) {
+#pragma unroll 1
+  for (int k = 0; k < DP / 32; ++k) {
+    uint32_t o[32];
+    if (have) {
+      tmem_ld32(taddr + 32 * k, o);
+      tmem_wait_ld_dep(o);
+    }
+    if (live) {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = some ? o[x] : 0u;
+      if (rec) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          *reinterpret_cast<uint4*>(rec + 32 * k + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+      } else if (32 * k < D) {
+        store_bf16x32(out + 32 * k, o, f, 32 * k, D);
+      }
+    }
+    __syncwarp();   // the warp's lanes load together
+  }
+}
+
+// ---------------------------------------------------------------- dK, dV
+
+template <int DP>
+struct DkvLayout {
+  using T = Tile<DP>;
+  // ring of Q and dY tiles in the order Q0 dY0 Q1 dY1 ...
+  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 9 : 14;
+  static constexpr int NB = 2;   // buffers of (nl, delta)
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = T::BYTES;
+  static constexpr int RING_OFF = 2 * T::BYTES;
+  static constexpr int NL_OFF = RING_OFF + SLOTS * T::BYTES;       // [NB][nl 128, delta 128]
+  static constexpr int BAR_OFF = NL_OFF + NB * 1024;
+  static constexpr int NBARS = 2 * SLOTS + 1 + 2 * NB + 4 + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int BYTES = MISC_OFF + 16;
+};
+
+template <int KS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ AttnBwdArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int DP = attn_dp(16 * KS);
+  using L = DkvLayout<DP>;
+  using T = Tile<DP>;
+  constexpr int NS = L::SLOTS, NB = L::NB;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
+  uint64_t* full = bars;               // [slot] tile landed
+  uint64_t* empty = bars + NS;         // [slot] its last product is done
+  uint64_t* kv_full = bars + 2 * NS;
+  uint64_t* nl_full = kv_full + 1;     // [NB]
+  uint64_t* nl_empty = nl_full + NB;   // [NB]
+  uint64_t* s_full = nl_empty + NB;
+  uint64_t* p_ready = s_full + 1;
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_ready = s_full + 3;
+  uint64_t* done = s_full + 4;
+  uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
+  volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
+  constexpr uint32_t TS = 0, TP = 128, TK = 256, TV = 256 + DP;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's work
+  int64_t u = blockIdx.x;
+  const int split = (int)(u % A.dkv_splits);
+  u /= A.dkv_splits;
+  int kt;
+  int64_t bh;
+  if (A.causal) {   // the keys that most queries see first
+    const int64_t BH = (int64_t)A.B * A.Hk;
+    kt = (int)(u / BH);
+    bh = u % BH;
+  } else {
+    kt = (int)(u % A.ktiles);
+    bh = u / A.ktiles;
+  }
+  const int b = (int)(bh / A.Hk), hk = (int)(bh % A.Hk), G = A.Hq / A.Hk;
+  const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
+  const int k0 = kt * kAttnTile;
+  const int krow0 = tile_row0(kt, kAttnTile, sq.kl);
+  const int first = sq.first_query_tile(k0, kAttnTile);
+  const int per = k0 < sq.kl ? max(0, (sq.ql + kAttnTile - 1) / kAttnTile - first) : 0;
+  const int lo = (int)((int64_t)per * G * split / A.dkv_splits);
+  int n = (int)((int64_t)per * G * (split + 1) / A.dkv_splits) - lo;
+  if (smem_u32(smem) & 1023) {   // tiles and their descriptors need this alignment
+    n = 0;
+    if (threadIdx.x == 0) record_error(A.err, kErrAttnDkvTmaWait);
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2 * NS + 1; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(&nl_full[s], 32);
+      mbar_init(&nl_empty[s], 256);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_ready, 256);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 256);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kWarpTma) {
+    // --------------------------------------------------------------- TMA
+    if (lane == 0 && n > 0) {
+      const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
+      const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
+      const int qb = (A.bcast & 1) ? 0 : b, gb = (A.bcast & 64) ? 0 : b;
+      mbar_arrive_expect_tx(kv_full, 2 * T::BYTES);
+      load_tile<DP>(smem + L::K_OFF, &tmK, kv_full, krow0, kh, kb);
+      load_tile<DP>(smem + L::V_OFF, &tmV, kv_full, krow0, vh, vb);
+      int last = -1;
+      for (int it = 0; it < 2 * n; ++it) {
+        const int s = it % NS, use = it / NS;
+        if (use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) {
+          record_error(A.err, kErrAttnDkvTmaWait);
+          *abort_flag = 1;
+          break;
+        }
+        if (*abort_flag) break;
+        const int x = lo + (it >> 1);
+        const int h = hk * G + x / per;
+        const int row = tile_row0(first + x % per, kAttnTile, sq.ql);
+        uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
+        mbar_arrive_expect_tx(&full[s], T::BYTES);
+        if (it & 1) load_tile<DP>(dst, &tmG, &full[s], row, (A.bcast & 128) ? 0 : h, gb);
+        else load_tile<DP>(dst, &tmQ, &full[s], row, (A.bcast & 8) ? 0 : h, qb);
+        last = it;
+      }
+      // every load lands before the CTA can exit
+      for (int it = max(0, last - NS + 1); it <= last; ++it)
+        mbar_wait_sleep(&full[it % NS], (uint32_t)((it / NS) & 1));
+      mbar_wait_sleep(kv_full, 0);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // --------------------------------------------------------------- MMA
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
+      const uint64_t dK = T::k_major(smem_u32(smem + L::K_OFF));
+      const uint64_t dV = T::k_major(smem_u32(smem + L::V_OFF));
+      const uint32_t ring = smem_u32(smem + L::RING_OFF);
+      const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
+      auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
+      auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
+      // S^T or dP^T: A = keys' tile, B = ring tile
+      auto issue_nt = [&](uint32_t d, uint64_t a, int it, uint64_t* bar) {
+        const uint64_t bd = rK + slot(it);
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+          mma_ss(tmem + d, a + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+        mma_commit(bar);
+      };
+      // dV or dK: A = P^T or dS^T in TMEM, B = ring tile, 128 queries deep
+      auto issue_nn = [&](uint32_t d, uint32_t a, int it, bool start) {
+        const uint64_t bd = rM + slot(it);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + d, tmem + a + a_step(kk), bd + kk * T::MN_STEP, idD,
+                 (!start || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[it % NS]);
+      };
+      bool ok = mbar_wait(kv_full, 0) && landed(0) && landed(1);
+      if (ok) {
+        tc_fence_after();
+        issue_nt(TS, dK, 0, s_full);
+        issue_nt(TP, dV, 1, dp_full);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = mbar_wait(p_ready, (uint32_t)(j & 1)))) break;
+        tc_fence_after();
+        issue_nn(TV, TS, 2 * j + 1, j == 0);
+        if (j + 1 < n) {
+          if (!(ok = landed(2 * j + 2))) break;
+          tc_fence_after();
+          issue_nt(TS, dK, 2 * j + 2, s_full);
+        }
+        if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
+        tc_fence_after();
+        issue_nn(TK, TP, 2 * j, j == 0);
+        if (j + 1 < n) {
+          if (!(ok = landed(2 * j + 3))) break;
+          tc_fence_after();
+          issue_nt(TP, dV, 2 * j + 3, dp_full);
+        }
+        if (*abort_flag) ok = false;
+      }
+      if (!ok) {
+        record_error(A.err, kErrAttnDkvMmaWait);
+        *abort_flag = 1;
+      }
+      mma_commit(done);
+      mbar_wait_sleep(done, 0);
+    }
+    __syncwarp();
+  } else if (warp == kWarpAux) {
+    // --------------------------- nl and delta of each tile's 128 columns
+    // Columns before the tile's own queries (a last tile moved back) get
+    // nl = -inf: weight 0.
+    bool ok = true;
+    for (int j = 0; ok && j < n; ++j) {
+      const int s = j % NB, use = j / NB;
+      if (use > 0) ok = warp_all(mbar_wait_sleep(&nl_empty[s], (uint32_t)((use - 1) & 1)));
+      if (!ok) break;
+      const int x = lo + j, t = first + x % per;
+      const int row0 = tile_row0(t, kAttnTile, sq.ql);
+      const int64_t base = ((int64_t)b * A.Hq + hk * G + x / per) * A.Nq;
+      float* dst = (float*)(smem + L::NL_OFF + s * 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = 32 * k + lane, q = row0 + col;
+        const bool own = q >= t * kAttnTile;
+        dst[col] = own ? A.nl[base + q] : -INFINITY;
+        dst[128 + col] = own ? A.delta[base + q] : 0.f;
+      }
+      mbar_arrive(&nl_full[s]);
+    }
+    if (!ok) {
+      record_error(A.err, kErrAttnDkvRowWait);
+      *abort_flag = 1;
+    }
+  } else if (warp < 8) {
+    // ----------------------------------------------------- softmax warps
+    const int w = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;   // TMEM lane: key krow0 + r
+    const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lb + TS + 64 * w, tP = tmem + lb + TP + 64 * w;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int s = j % NB;
+      const int x = lo + j, t = first + x % per;
+      const int row0 = tile_row0(t, kAttnTile, sq.ql);
+      // columns below cl do not see this lane's key
+      const int cl = sq.causal ? krow0 + r - sq.off - row0 - 64 * w : -1;
+      const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + 64 * w;
+      if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((j / NB) & 1)) &&
+                    mbar_wait(s_full, (uint32_t)(j & 1)))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      uint32_t p[64];
+      tmem_ld64(tS, p);
+      tmem_wait_ld_dep64(p);
+      // a tile with masked columns or rows without weight keeps to the MUFU,
+      // whose exponential of -inf is 0
+      const bool gone = nl[lane] == -INFINITY || nl[32 + lane] == -INFINITY;
+      if (warp_any(cl > 0 || gone)) {
+        mask_cols(p, 0, cl, 63);
+        exp64<true, 0>(p, A.c, 0.f, nl);
+      } else {
+        exp64<true, kBwdPoly>(p, A.c, 0.f, nl);
+      }
+      store_bf16_tmem(tS, p);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_ready);
+      if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      uint32_t g[64];
+      tmem_ld64(tP, g);
+      tmem_wait_ld_dep64(g);
+      ds64<true>(g, p, 0.f, nl + 128);
+      mbar_arrive(&nl_empty[s]);
+      store_bf16_tmem(tP, g);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
+    if (!ok) {
+      record_error(A.err, kErrAttnDkvRowWait);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    tc_fence_after();
+    // warpgroup 0 stores dK, warpgroup 1 dV: this tile's own keys, then
+    // zeros for the rows past the length
+    const int key = krow0 + r;
+    const Tok& to = w ? A.dv : A.dk;
+    __nv_bfloat16* out = (__nv_bfloat16*)(w ? A.dV : A.dK) + b * to.sb + hk * to.sh;
+    float* rec = nullptr;
+    if (A.dkv_splits > 1)
+      rec = A.dkv_part + (((bh * A.ktiles + kt) * A.dkv_splits + split) * 2 + w) * (int64_t)kAttnTile * DP;
+    const bool own = key >= k0 && key < sq.kl;
+    put_row<DP>(tmem + lb + (w ? TV : TK), n > 0, n > 0, w ? 1.f : A.scale, out + key * to.sn,
+                rec ? rec + (int64_t)(key - k0) * DP : nullptr, own, A.D);
+    if (!rec && k0 + r >= sq.kl && k0 + r < A.Nk)
+      for (int d = 0; d < A.D; d += 8)
+        *reinterpret_cast<uint4*>(out + (k0 + r) * to.sn + d) = make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// -------------------------------------------------------------------- dQ
+
+template <int DP>
+struct DqLayout {
+  using T = Tile<DP>;
+  // ring of K and V tiles in the order K0 V0 K1 V1 ...
+  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 9 : 14;
+  static constexpr int Q_OFF = 0;
+  static constexpr int G_OFF = T::BYTES;
+  static constexpr int RING_OFF = 2 * T::BYTES;
+  static constexpr int BAR_OFF = RING_OFF + SLOTS * T::BYTES;
+  static constexpr int NBARS = 2 * SLOTS + 1 + 2 + 2 + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int BYTES = MISC_OFF + 16;
+};
+
+template <int KS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                   const __grid_constant__ AttnBwdArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int DP = attn_dp(16 * KS);
+  using L = DqLayout<DP>;
+  using T = Tile<DP>;
+  constexpr int NS = L::SLOTS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + NS;
+  uint64_t* q_full = bars + 2 * NS;
+  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_ready = s_full + 3;
+  uint64_t* done = s_full + 4;
+  uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
+  volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
+  constexpr uint32_t TP = 256, TQ = 384;   // S: 0 and 128
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's work
+  int64_t u = blockIdx.x;
+  const int split = (int)(u % A.dq_splits);
+  u /= A.dq_splits;
+  int qt;
+  int64_t bh;
+  if (A.causal) {   // longest rows first
+    const int64_t BH = (int64_t)A.B * A.Hq;
+    qt = A.qtiles - 1 - (int)(u / BH);
+    bh = u % BH;
+  } else {
+    qt = (int)(u % A.qtiles);
+    bh = u / A.qtiles;
+  }
+  const int b = (int)(bh / A.Hq), h = (int)(bh % A.Hq), hk = h / (A.Hq / A.Hk);
+  const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
+  const int q0 = qt * kAttnTile;
+  const int nall = q0 < sq.ql ? sq.key_tiles(q0 + kAttnTile - 1, kAttnTile) : 0;
+  const int lo = (int)((int64_t)nall * split / A.dq_splits);
+  int n = (int)((int64_t)nall * (split + 1) / A.dq_splits) - lo;
+  if (smem_u32(smem) & 1023) {   // tiles and their descriptors need this alignment
+    n = 0;
+    if (threadIdx.x == 0) record_error(A.err, kErrAttnDqTmaWait);
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2 * NS + 1; ++s) mbar_init(&bars[s], 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 256);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kWarpTma) {
+    // --------------------------------------------------------------- TMA
+    if (lane == 0 && n > 0) {
+      const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
+      const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
+      mbar_arrive_expect_tx(q_full, 2 * T::BYTES);
+      load_tile<DP>(smem + L::Q_OFF, &tmQ, q_full, q0, (A.bcast & 8) ? 0 : h, (A.bcast & 1) ? 0 : b);
+      load_tile<DP>(smem + L::G_OFF, &tmG, q_full, q0, (A.bcast & 128) ? 0 : h,
+                    (A.bcast & 64) ? 0 : b);
+      int last = -1;
+      for (int it = 0; it < 2 * n; ++it) {
+        const int s = it % NS, use = it / NS;
+        if (use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) {
+          record_error(A.err, kErrAttnDqTmaWait);
+          *abort_flag = 1;
+          break;
+        }
+        if (*abort_flag) break;
+        const int row = tile_row0(lo + (it >> 1), kAttnTile, sq.kl);
+        uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
+        mbar_arrive_expect_tx(&full[s], T::BYTES);
+        if (it & 1) load_tile<DP>(dst, &tmV, &full[s], row, vh, vb);
+        else load_tile<DP>(dst, &tmK, &full[s], row, kh, kb);
+        last = it;
+      }
+      for (int it = max(0, last - NS + 1); it <= last; ++it)
+        mbar_wait_sleep(&full[it % NS], (uint32_t)((it / NS) & 1));
+      mbar_wait_sleep(q_full, 0);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // --------------------------------------------------------------- MMA
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
+      const uint64_t dQ = T::k_major(smem_u32(smem + L::Q_OFF));
+      const uint64_t dG = T::k_major(smem_u32(smem + L::G_OFF));
+      const uint32_t ring = smem_u32(smem + L::RING_OFF);
+      const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
+      auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
+      auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
+      auto issue_S = [&](int j) {
+        const uint64_t bd = rK + slot(2 * j);
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+          mma_ss(tmem + 128 * (j & 1), dQ + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+        mma_commit(&s_full[j & 1]);
+      };
+      auto issue_dP = [&](int j) {
+        const uint64_t bd = rK + slot(2 * j + 1);
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+          mma_ss(tmem + TP, dG + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+        mma_commit(dp_full);
+        mma_commit(&empty[(2 * j + 1) % NS]);
+      };
+      auto issue_dQ = [&](int j) {
+        const uint64_t bd = rM + slot(2 * j);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + TQ, tmem + TP + a_step(kk), bd + kk * T::MN_STEP, idD,
+                 (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[(2 * j) % NS]);
+      };
+      bool ok = mbar_wait(q_full, 0) && landed(0) && landed(1);
+      if (ok) {
+        tc_fence_after();
+        issue_S(0);
+        issue_dP(0);
+      }
+      if (ok && n > 1 && (ok = landed(2))) {
+        tc_fence_after();
+        issue_S(1);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
+        tc_fence_after();
+        issue_dQ(j);
+        if (j + 1 < n) {
+          if (!(ok = landed(2 * j + 3))) break;
+          tc_fence_after();
+          issue_dP(j + 1);
+        }
+        if (j + 2 < n) {
+          if (!(ok = landed(2 * j + 4))) break;
+          tc_fence_after();
+          issue_S(j + 2);
+        }
+        if (*abort_flag) ok = false;
+      }
+      if (!ok) {
+        record_error(A.err, kErrAttnDqMmaWait);
+        *abort_flag = 1;
+      }
+      mma_commit(done);
+      mbar_wait_sleep(done, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ----------------------------------------------------- softmax warps
+    const int w = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tP = tmem + lb + TP + 64 * w;
+    const int i = q0 + r;
+    const bool live = i < A.Nq;
+    const int64_t row = bh * A.Nq + i;
+    const float nl = live && i < sq.ql ? A.nl[row] : -INFINITY;
+    const float delta = live && i < sq.ql ? A.delta[row] : 0.f;
+    const bool gone = nl == -INFINITY;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int t = lo + j;
+      const int row0 = tile_row0(t, kAttnTile, sq.kl);
+      const int cl = t * kAttnTile - row0 - 64 * w;
+      const int ch = (sq.causal ? i + sq.off - row0 : 127) - 64 * w;
+      if (!warp_all(mbar_wait(&s_full[j & 1], (uint32_t)((j >> 1) & 1)))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      uint32_t p[64];
+      tmem_ld64(tmem + lb + 128 * (j & 1) + 64 * w, p);
+      tmem_wait_ld_dep64(p);
+      if (warp_any(cl > 0 || ch < 63 || gone)) {
+        mask_cols(p, 0, cl, ch);
+        exp64<false, 0>(p, A.c, nl, nullptr);
+      } else {
+        exp64<false, kBwdPoly>(p, A.c, nl, nullptr);
+      }
+      if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      uint32_t g[64];
+      tmem_ld64(tP, g);
+      tmem_wait_ld_dep64(g);
+      ds64<false>(g, p, delta, nullptr);
+      store_bf16_tmem(tP, g);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
+    if (!ok) {
+      record_error(A.err, kErrAttnDqRowWait);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    tc_fence_after();
+    if (w == 0) {
+      __nv_bfloat16* out = (__nv_bfloat16*)A.dQ + b * A.dq.sb + h * A.dq.sh + i * A.dq.sn;
+      float* rec = nullptr;
+      if (A.dq_splits > 1)
+        rec = A.dq_part + (((bh * A.qtiles + qt) * A.dq_splits + split) * kAttnTile + r) * (int64_t)DP;
+      put_row<DP>(tmem + lb + TQ, n > 0, n > 0 && !gone, A.scale, out, rec, live, A.D);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int KS>
+cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
+  constexpr int DP = attn_dp(16 * KS);
+  CUtensorMap mq, mk, mv, mg;
+  cudaError_t e;
+  if ((e = attn_map(&mq, a.Q, d.q, d.B, d.Hq, d.Nq, d.D, DP, 128, 1)) != cudaSuccess) return e;
+  if ((e = attn_map(&mk, a.K, d.k, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
+  if ((e = attn_map(&mv, a.V, d.v, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
+  if ((e = attn_map(&mg, a.dY, d.dy, d.B, d.Hq, d.Nq, d.D, DP, 128, 1)) != cudaSuccess) return e;
+  auto go = [&](auto kernel, int64_t grid, int bytes) {
+    const int smem = bytes > kMinSmemBytes ? bytes : kMinSmemBytes;
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) return r;
+    r = launch_pdl(kernel, dim3((unsigned)grid), kThreads, smem, st, mq, mk, mv, mg, a);
+    return r != cudaSuccess ? r : cudaPeekAtLastError();
+  };
+  if (a.dK && (e = go(attn_dkv_kernel<KS>, p.dkv_units * p.dkv_splits, DkvLayout<DP>::BYTES)) !=
+                  cudaSuccess)
+    return e;
+  if (a.dQ) e = go(attn_dq_kernel<KS>, p.dq_units * p.dq_splits, DqLayout<DP>::BYTES);
+  return e;
+}
+
+}  // namespace
+}  // namespace attn
+
+cudaError_t launch_attn_bwd_tc(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
+                               cudaStream_t st) {
+  using namespace attn;
+  switch (attn_ks(d.D)) {
+    case 2: return bwd_t<2>(d, p, a, st);
+    case 4: return bwd_t<4>(d, p, a, st);
+    case 5: return bwd_t<5>(d, p, a, st);
+    case 6: return bwd_t<6>(d, p, a, st);
+    default: return bwd_t<8>(d, p, a, st);
+  }
+}
+
+}  // namespace flare
