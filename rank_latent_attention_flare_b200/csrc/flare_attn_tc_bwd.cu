@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpTma) {
     // --------------------------------------------------------------- TMA
-    if (lane == 0 && n > 0) {
+    if (n > 0 && elect_one()) {
       const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
       const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
       const int qb = (A.bcast & 1) ? 0 : b, gb = (A.bcast & 64) ? 0 : b;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0 && n > 0) {
+    if (n > 0 && elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
       const uint64_t dK = T::k_major(smem_u32(smem + L::K_OFF));
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpTma) {
     // --------------------------------------------------------------- TMA
-    if (lane == 0 && n > 0) {
+    if (n > 0 && elect_one()) {
       const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
       const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
       mbar_arrive_expect_tx(q_full, 2 * T::BYTES);
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0 && n > 0) {
+    if (n > 0 && elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
       const uint64_t dQ = T::k_major(smem_u32(smem + L::Q_OFF));

@@ -21,6 +21,8 @@
 // O at 256 + DP w.  All MMAs are issued by one thread, in batches whose
 // length is a compile-time constant (KS steps over D): a product under a
 // run-time condition of its own reached the tensor core with wrong operands.
+// They run in the order of issue, so that S of the next tile may be issued
+// behind the product that reads P from the same columns.
 //
 // Bound: per tile and SM the tensor core needs 4 D clocks for each of the two
 // products and the MUFU 1024 clocks for the exponentials, so D = 128 is bound
@@ -150,9 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
+    regs_release<kRegsProducer>();
     if (warp == kWarpTma) {
       // ------------------------------------------------------------- TMA
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------- MMA
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t idPV = idesc_bf16_f32(128, 16 * KS, 0, 1);
         const uint32_t kv0 = smem_u32(smem + L::KV_OFF);
@@ -246,11 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = mbar_wait(&p_ready[w], (uint32_t)(j & 1)))) break;
               tc_fence_after();
               issue_PV(w, j, j == 0);
-              if (j + 1 < nw) {   // its S replaces the P that the product reads
-                if (!(ok = mbar_wait(&pv_done[w], (uint32_t)(j & 1)))) break;
-                tc_fence_after();
-                issue_S(w, j + 1);
-              }
+              if (j + 1 < nw) issue_S(w, j + 1);
             }
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
             if (j + 1 < n) mma_commit(&kv_empty[item_k<QT>(j + 1) % NS]);
@@ -271,9 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_PV(w, j, j < 2);
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
             if (j + 2 < n) {
-              // its S replaces the P that the product reads
-              if (!(ok = full(item_k<QT>(j + 2)) && mbar_wait(&pv_done[w], (uint32_t)((j >> 1) & 1))))
-                break;
+              if (!(ok = full(item_k<QT>(j + 2)))) break;
               tc_fence_after();
               issue_S(w, j + 2);
               mma_commit(&kv_empty[item_k<QT>(j + 2) % NS]);
@@ -292,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- softmax
+    regs_acquire<kRegsCompute>();
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;               // TMEM lane
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
@@ -329,18 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cl = t * kAttnTile - row0;
       const int ch = sq.causal ? i + sq.off - row0 : 127;
       const bool masked = warp_any(cl > 0 || ch < 127);
-      // The maximum over both halves; the second half is read again after the
-      // first half's P is written (over the first half's S, held in registers).
-      uint32_t a[64];
+      uint32_t a[2][64];
+      tmem_ld64(tS, a[0]);
+      tmem_ld64(tS + 64, a[1]);
+      tmem_wait_ld_dep128(a[0], a[1]);
+      if (masked) {
+        mask_cols(a[0], 0, cl, ch);
+        mask_cols(a[1], 64, cl, ch);
+      }
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      tmem_ld64(tS + 64, a);
-      tmem_wait_ld_dep64(a);
-      if (masked) mask_cols(a, 64, cl, ch);
-      max_fold64(a, m4);
-      tmem_ld64(tS, a);
-      tmem_wait_ld_dep64(a);
-      if (masked) mask_cols(a, 0, cl, ch);
-      max_fold64(a, m4);
+      max_fold64(a[0], m4);
+      max_fold64(a[1], m4);
       const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
       const bool move = (mx - mr) * A.c > kRescaleTau;
       if (warp_any(move)) {
@@ -369,20 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float neg = mr == -INFINITY ? 0.f : -mr * A.c;
       float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (k == 1) {
-          tmem_ld64(tS + 64, a);
-          tmem_wait_ld_dep64(a);
-          if (masked) mask_cols(a, 64, cl, ch);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t pk[16];
-          // masked tiles: the MUFU's exponential maps -inf to exactly 0
-          if (masked) exp_pack_pairs<16, 0>(a + 32 * x, A.c, neg, pk, s4);
-          else exp_pack_pairs<16, fwd_poly<DP>()>(a + 32 * x, A.c, neg, pk, s4);
-          tmem_st16(tS + 32 * k + 16 * x, pk);
-        }
+      for (int k = 0; k < 4; ++k) {
+        uint32_t pk[16];
+        const uint32_t* x = a[k >> 1] + 32 * (k & 1);
+        // masked tiles: the MUFU's exponential maps -inf to exactly 0
+        if (masked) exp_pack_pairs<16, 0>(x, A.c, neg, pk, s4);
+        else exp_pack_pairs<16, fwd_poly<DP>()>(x, A.c, neg, pk, s4);
+        tmem_st16(tS + 16 * k, pk);
       }
       tmem_wait_st();
       tc_fence_before();
