@@ -9,7 +9,7 @@
 //   S^T = K Q^T,  P^T = 2^(c S^T + nl),   dV += P^T dY     (P^T from TMEM)
 //   dP^T = V dY^T, dS^T = P^T (dP^T - delta), dK += dS^T Q
 // nl = -lse and delta differ by column: they come from shared memory.
-// Warpgroup w computes columns [64 w, 64 w + 64).  P^T and dS^T (bf16)
+// Warpgroup w computes columns [32 w, 32 w + 32).  P^T and dS^T (bf16)
 // replace the columns of S^T and dP^T that the same warp has read.  The
 // MMAs alternate with the softmax so that the tensor core always has two
 // products to run: {dV_j, S_j+1} while dS_j is computed, {dK_j, dP_j+1}
@@ -36,13 +36,20 @@ namespace {
 // Every k-th pair of exponentials on the FMA pipe (tiles without a mask).
 constexpr int kBwdPoly = 3;
 
-// 2^(c a + n) for 64 values, in place, n[] per value (column) or one for all:
+// 16 softmax warps: warpgroup w of four takes 32 of a tile's 128 columns, so
+// that four warps on each SM sub-partition hide each other's latencies (with
+// eight warps of 64 columns the causal training step took 562 us).
+constexpr int kBThreads = 640;
+constexpr int kBWarpTma = 16, kBWarpMma = 17, kBWarpAux = 18;
+constexpr int kCols = 32;
+
+// 2^(c a + n) for a lane's columns, in place, n[] per column or one for all:
 // probabilities in float32.
 template <bool COLS, int POLY>
-__device__ __forceinline__ void exp64(uint32_t (&a)[64], float c, float n, const float* cols) {
+__device__ __forceinline__ void exp_cols(uint32_t (&a)[kCols], float c, float n, const float* cols) {
   const uint64_t c2 = f32x2(c, c);
 #pragma unroll
-  for (int t = 0; t < 64; t += 4) {
+  for (int t = 0; t < kCols; t += 4) {
     float4 v;
     if (COLS) v = *reinterpret_cast<const float4*>(cols + t);
     else v = make_float4(n, n, n, n);
@@ -65,24 +72,21 @@ __device__ __forceinline__ void exp64(uint32_t (&a)[64], float c, float n, const
   }
 }
 
-// 32 packed bf16 pairs of 64 values to TMEM.
-__device__ __forceinline__ void store_bf16_tmem(uint32_t taddr, const uint32_t (&a)[64]) {
+// A lane's columns as packed bf16 pairs to TMEM.
+__device__ __forceinline__ void store_bf16_tmem(uint32_t taddr, const uint32_t (&a)[kCols]) {
+  uint32_t pk[kCols / 2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      pk[t] = pack_bf16(__uint_as_float(a[32 * h + 2 * t]), __uint_as_float(a[32 * h + 2 * t + 1]));
-    tmem_st16(taddr + 16 * h, pk);
-  }
+  for (int t = 0; t < kCols / 2; ++t)
+    pk[t] = pack_bf16(__uint_as_float(a[2 * t]), __uint_as_float(a[2 * t + 1]));
+  tmem_st16(taddr, pk);
 }
 
 // dS = P (dP - delta), in place in g (dP on entry).
 template <bool COLS>
-__device__ __forceinline__ void ds64(uint32_t (&g)[64], const uint32_t (&p)[64], float d,
+__device__ __forceinline__ void ds_cols(uint32_t (&g)[kCols], const uint32_t (&p)[kCols], float d,
                                      const float* cols) {
 #pragma unroll
-  for (int t = 0; t < 64; t += 4) {
+  for (int t = 0; t < kCols; t += 4) {
     float4 v;
     if (COLS) v = *reinterpret_cast<const float4*>(cols + t);
     else v = make_float4(d, d, d, d);
@@ -101,17 +105,20 @@ __device__ __forceinline__ void ds64(uint32_t (&g)[64], const uint32_t (&p)[64],
   }
 }
 
-// TMEM column of K step kk (16 rows) of a bf16 operand stored by two
-// warpgroups, each in the first half of its own 64 columns.
-__device__ __forceinline__ constexpr uint32_t a_step(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }
+// TMEM column of K step kk (16 rows) of a bf16 operand stored by the
+// warpgroups, each in the first half of its own columns.
+__device__ __forceinline__ constexpr uint32_t a_step(int kk) {
+  return kCols * (kk / (kCols / 16)) + 8 * (kk % (kCols / 16));
+}
 
-// One lane's row of an accumulator of DP columns: as bf16 times f to `out`
-// (columns below D), or as float32 to a record, or zeros.  Whole-warp call.
+// One lane's row of an accumulator of DP columns, every step-th block of 32
+// from the first: as bf16 times f to `out` (columns below D), or as float32
+// to a record, or zeros.  Whole-warp call.
 template <int DP>
-__device__ __forceinline__ void put_row(uint32_t taddr, bool have, bool some, float f,
-                                        __nv_bfloat16* out, float* rec, bool live, int D) {
+__device__ __forceinline__ void put_row(uint32_t taddr, int first, int step, bool have, bool some,
+                                        float f, __nv_bfloat16* out, float* rec, bool live, int D) {
 #pragma unroll 1
-  for (int k = 0; k < DP / 32; ++k) {
+  for (int k = first; k < DP / 32; k += step) {
     uint32_t o[32];
     if (have) {
       tmem_ld32(taddr + 32 * k, o);
@@ -151,7 +158,7 @@ struct DkvLayout {
 };
 
 template <int KS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                     const __grid_constant__ AttnBwdArgs A) {
@@ -210,23 +217,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2 * NS + 1; ++s) mbar_init(&bars[s], 1);
     for (int s = 0; s < NB; ++s) {
       mbar_init(&nl_full[s], 32);
-      mbar_init(&nl_empty[s], 256);
+      mbar_init(&nl_empty[s], 512);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_ready, 256);
+    mbar_init(p_ready, 512);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 256);
+    mbar_init(ds_ready, 512);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
+  if (warp == kBWarpMma) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kWarpTma) {
+  if (warp == kBWarpTma) {
     // --------------------------------------------------------------- TMA
     if (n > 0 && elect_one()) {
       const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_sleep(kv_full, 0);
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
+  } else if (warp == kBWarpMma) {
     // --------------------------------------------------------------- MMA
     if (n > 0 && elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_sleep(done, 0);
     }
     __syncwarp();
-  } else if (warp == kWarpAux) {
+  } else if (warp == kBWarpAux) {
     // --------------------------- nl and delta of each tile's 128 columns
     // Columns before the tile's own queries (a last tile moved back) get
     // nl = -inf: weight 0.
@@ -346,20 +353,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       record_error(A.err, kErrAttnDkvRowWait);
       *abort_flag = 1;
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ----------------------------------------------------- softmax warps
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;   // TMEM lane: key krow0 + r
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lb + TS + 64 * w, tP = tmem + lb + TP + 64 * w;
+    const uint32_t tS = tmem + lb + TS + kCols * w, tP = tmem + lb + TP + kCols * w;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int s = j % NB;
       const int x = lo + j, t = first + x % per;
       const int row0 = tile_row0(t, kAttnTile, sq.ql);
       // columns below cl do not see this lane's key
-      const int cl = sq.causal ? krow0 + r - sq.off - row0 - 64 * w : -1;
-      const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + 64 * w;
+      const int cl = sq.causal ? krow0 + r - sq.off - row0 - kCols * w : -1;
+      const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
       if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((j / NB) & 1)) &&
                     mbar_wait(s_full, (uint32_t)(j & 1)))) {
         ok = false;
@@ -367,17 +374,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       tc_fence_after();
-      uint32_t p[64];
-      tmem_ld64(tS, p);
-      tmem_wait_ld_dep64(p);
+      uint32_t p[kCols];
+      tmem_ld32(tS, p);
+      tmem_wait_ld_dep(p);
       // a tile with masked columns or rows without weight keeps to the MUFU,
       // whose exponential of -inf is 0
-      const bool gone = nl[lane] == -INFINITY || nl[32 + lane] == -INFINITY;
+      const bool gone = nl[lane] == -INFINITY;
       if (warp_any(cl > 0 || gone)) {
-        mask_cols(p, 0, cl, 63);
-        exp64<true, 0>(p, A.c, 0.f, nl);
+        mask_cols(p, 0, cl, kCols - 1);
+        exp_cols<true, 0>(p, A.c, 0.f, nl);
       } else {
-        exp64<true, kBwdPoly>(p, A.c, 0.f, nl);
+        exp_cols<true, kBwdPoly>(p, A.c, 0.f, nl);
       }
       store_bf16_tmem(tS, p);
       tmem_wait_st();
@@ -389,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       tc_fence_after();
-      uint32_t g[64];
-      tmem_ld64(tP, g);
-      tmem_wait_ld_dep64(g);
-      ds64<true>(g, p, 0.f, nl + 128);
+      uint32_t g[kCols];
+      tmem_ld32(tP, g);
+      tmem_wait_ld_dep(g);
+      ds_cols<true>(g, p, 0.f, nl + 128);
       mbar_arrive(&nl_empty[s]);
       store_bf16_tmem(tP, g);
       tmem_wait_st();
@@ -406,18 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     tc_fence_after();
-    // warpgroup 0 stores dK, warpgroup 1 dV: this tile's own keys, then
+    // warpgroups 0 and 1 store dK, 2 and 3 dV: this tile's own keys, then
     // zeros for the rows past the length
-    const int key = krow0 + r;
-    const Tok& to = w ? A.dv : A.dk;
-    __nv_bfloat16* out = (__nv_bfloat16*)(w ? A.dV : A.dK) + b * to.sb + hk * to.sh;
+    const int key = krow0 + r, v = w >> 1;
+    const Tok& to = v ? A.dv : A.dk;
+    __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + b * to.sb + hk * to.sh;
     float* rec = nullptr;
     if (A.dkv_splits > 1)
-      rec = A.dkv_part + (((bh * A.ktiles + kt) * A.dkv_splits + split) * 2 + w) * (int64_t)kAttnTile * DP;
+      rec = A.dkv_part + (((bh * A.ktiles + kt) * A.dkv_splits + split) * 2 + v) * (int64_t)kAttnTile * DP;
     const bool own = key >= k0 && key < sq.kl;
-    put_row<DP>(tmem + lb + (w ? TV : TK), n > 0, n > 0, w ? 1.f : A.scale, out + key * to.sn,
-                rec ? rec + (int64_t)(key - k0) * DP : nullptr, own, A.D);
-    if (!rec && k0 + r >= sq.kl && k0 + r < A.Nk)
+    put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, n > 0, n > 0, v ? 1.f : A.scale,
+                out + key * to.sn, rec ? rec + (int64_t)(key - k0) * DP : nullptr, own, A.D);
+    if ((w & 1) && !rec && k0 + r >= sq.kl && k0 + r < A.Nk)
       for (int d = 0; d < A.D; d += 8)
         *reinterpret_cast<uint4*>(out + (k0 + r) * to.sn + d) = make_uint4(0, 0, 0, 0);
   }
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kBWarpMma) tmem_dealloc(tmem, 512);
 }
 
 // -------------------------------------------------------------------- dQ
@@ -445,7 +452,7 @@ struct DqLayout {
 };
 
 template <int KS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBThreads, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                    const __grid_constant__ AttnBwdArgs A) {
@@ -500,18 +507,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 256);
+    mbar_init(ds_ready, 512);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) tmem_alloc(tmem_slot, 512);
+  if (warp == kBWarpMma) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kWarpTma) {
+  if (warp == kBWarpTma) {
     // --------------------------------------------------------------- TMA
     if (n > 0 && elect_one()) {
       const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_sleep(q_full, 0);
     }
     __syncwarp();
-  } else if (warp == kWarpMma) {
+  } else if (warp == kBWarpMma) {
     // --------------------------------------------------------------- MMA
     if (n > 0 && elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
@@ -609,12 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_sleep(done, 0);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ----------------------------------------------------- softmax warps
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tP = tmem + lb + TP + 64 * w;
+    const uint32_t tP = tmem + lb + TP + kCols * w;
     const int i = q0 + r;
     const bool live = i < A.Nq;
     const int64_t row = bh * A.Nq + i;
@@ -625,22 +632,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < n; ++j) {
       const int t = lo + j;
       const int row0 = tile_row0(t, kAttnTile, sq.kl);
-      const int cl = t * kAttnTile - row0 - 64 * w;
-      const int ch = (sq.causal ? i + sq.off - row0 : 127) - 64 * w;
+      const int cl = t * kAttnTile - row0 - kCols * w;
+      const int ch = (sq.causal ? i + sq.off - row0 : 127) - kCols * w;
       if (!warp_all(mbar_wait(&s_full[j & 1], (uint32_t)((j >> 1) & 1)))) {
         ok = false;
         break;
       }
       __syncwarp();
       tc_fence_after();
-      uint32_t p[64];
-      tmem_ld64(tmem + lb + 128 * (j & 1) + 64 * w, p);
-      tmem_wait_ld_dep64(p);
-      if (warp_any(cl > 0 || ch < 63 || gone)) {
+      uint32_t p[kCols];
+      tmem_ld32(tmem + lb + 128 * (j & 1) + kCols * w, p);
+      tmem_wait_ld_dep(p);
+      if (warp_any(cl > 0 || ch < kCols - 1 || gone)) {
         mask_cols(p, 0, cl, ch);
-        exp64<false, 0>(p, A.c, nl, nullptr);
+        exp_cols<false, 0>(p, A.c, nl, nullptr);
       } else {
-        exp64<false, kBwdPoly>(p, A.c, nl, nullptr);
+        exp_cols<false, kBwdPoly>(p, A.c, nl, nullptr);
       }
       if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
         ok = false;
@@ -648,10 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       tc_fence_after();
-      uint32_t g[64];
-      tmem_ld64(tP, g);
-      tmem_wait_ld_dep64(g);
-      ds64<false>(g, p, delta, nullptr);
+      uint32_t g[kCols];
+      tmem_ld32(tP, g);
+      tmem_wait_ld_dep(g);
+      ds_cols<false>(g, p, delta, nullptr);
       store_bf16_tmem(tP, g);
       tmem_wait_st();
       tc_fence_before();
@@ -664,19 +671,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     tc_fence_after();
-    if (w == 0) {
-      __nv_bfloat16* out = (__nv_bfloat16*)A.dQ + b * A.dq.sb + h * A.dq.sh + i * A.dq.sn;
-      float* rec = nullptr;
-      if (A.dq_splits > 1)
-        rec = A.dq_part + (((bh * A.qtiles + qt) * A.dq_splits + split) * kAttnTile + r) * (int64_t)DP;
-      put_row<DP>(tmem + lb + TQ, n > 0, n > 0 && !gone, A.scale, out, rec, live, A.D);
-    }
+    __nv_bfloat16* out = (__nv_bfloat16*)A.dQ + b * A.dq.sb + h * A.dq.sh + i * A.dq.sn;
+    float* rec = nullptr;
+    if (A.dq_splits > 1)
+      rec = A.dq_part + (((bh * A.qtiles + qt) * A.dq_splits + split) * kAttnTile + r) * (int64_t)DP;
+    put_row<DP>(tmem + lb + TQ, w, 4, n > 0, n > 0 && !gone, A.scale, out, rec, live, A.D);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kBWarpMma) tmem_dealloc(tmem, 512);
 }
 
 template <int KS>
@@ -692,7 +697,7 @@ cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
     const int smem = bytes > kMinSmemBytes ? bytes : kMinSmemBytes;
     cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (r != cudaSuccess) return r;
-    r = launch_pdl(kernel, dim3((unsigned)grid), kThreads, smem, st, mq, mk, mv, mg, a);
+    r = launch_pdl(kernel, dim3((unsigned)grid), kBThreads, smem, st, mq, mk, mv, mg, a);
     return r != cudaSuccess ? r : cudaPeekAtLastError();
   };
   if (a.dK && (e = go(attn_dkv_kernel<KS>, p.dkv_units * p.dkv_splits, DkvLayout<DP>::BYTES)) !=

@@ -17,8 +17,13 @@
 // query tiles do not fill the GPU, the key tiles are split over CTAs and the
 // records joined by attn_join_kernel in a fixed order.
 //
-// TMEM: S of warpgroup w at columns 128 w (its first 64 columns receive P),
-// O at 256 + DP w.  All MMAs are issued by one thread, in batches whose
+// TMEM: S of warpgroup w at columns 128 w, O at 256 + DP w.  P replaces the
+// first half of S: its first 64 keys are handed to the tensor core while the
+// others are computed, and S of the next tile follows the product.  With two
+// query tiles and D <= 64 there is room for P at 384 + 64 w: S of the next
+// tile is then computed as soon as the softmax has read S, so that the
+// softmax does not wait for the tensor core (D = 64, 16 heads of 4096
+// tokens, all pairs: 113 us instead of 123).  All MMAs are issued by one thread, in batches whose
 // length is a compile-time constant (KS steps over D): a product under a
 // run-time condition of its own reached the tensor core with wrong operands.
 // They run in the order of issue, so that S of the next tile may be issued
@@ -28,6 +33,8 @@
 // products and the MUFU 1024 clocks for the exponentials, so D = 128 is bound
 // by both about equally and smaller D by the exponentials; single-token
 // calls are bound by reading the keys and values once.
+#include <type_traits>
+
 #include "flare_attn_tc.cuh"
 
 namespace flare {
@@ -43,7 +50,7 @@ struct FwdLayout {
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = QT * T::BYTES;
   static constexpr int BAR_OFF = KV_OFF + STAGES * T::BYTES;
-  static constexpr int NBARS = 2 * STAGES + 1 + 2 + 2 + 2 + 1;
+  static constexpr int NBARS = 2 * STAGES + 1 + 2 + 2 + 2 + 2 + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int ML_OFF = MISC_OFF + 16;               // QT = 1: the second record's (ref, sum)
   static constexpr int BYTES = ML_OFF + 128 * 8;
@@ -51,9 +58,9 @@ struct FwdLayout {
   static_assert(STAGES * T::BYTES >= 128 * DP * 4, "exchange area");
 };
 
-// Every k-th pair of exponentials on the FMA pipe.
-template <int DP>
-__host__ __device__ constexpr int fwd_poly() { return DP == 128 ? 4 : 3; }
+// Every third pair of exponentials runs on the FMA pipe (2, 4 and none: 2 to
+// 7% slower at 4096 tokens).
+constexpr int kFwdPoly = 3;
 
 // Ring order of the key and value tiles: the order in which the MMAs use
 // them.  QT = 2: K0 V0 K1 V1 ...; QT = 1 runs two key tiles ahead: K0 K1 V0
@@ -77,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = FwdLayout<DP, QT>;
   using T = Tile<DP>;
   constexpr int NS = L::STAGES;
+  constexpr bool APART = QT == 2 && DP <= 64;   // P apart from S
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
@@ -86,7 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = q_full + 1;     // [w] S written by the MMA
   uint64_t* p_ready = s_full + 2;    // [w] S read and P written by the softmax
   uint64_t* pv_done = p_ready + 2;   // [w] O holds the tile
-  uint64_t* drain = pv_done + 2;
+  // [w] S read (P apart from S), or the first half of P written
+  uint64_t* early = pv_done + 2;
+  uint64_t* drain = early + 2;
   uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
   volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
 
@@ -138,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[w], 1);
       mbar_init(&p_ready[w], 128);
       mbar_init(&pv_done[w], 1);
+      mbar_init(&early[w], 128);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -224,13 +235,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + 128 * w, dQ + qo + T::kstep(kk), dK + ko + T::kstep(kk), idS, kk > 0);
           mma_commit(&s_full[w]);
         };
-        auto issue_PV = [&](int w, int j, bool first) {
+        const uint32_t P0 = tmem + (APART ? 384 : 0), PW = APART ? 64 : 128;
+        // O += P V over the keys [64 half, 64 half + 64) of tile j
+        auto issue_PV = [&](int w, int j, int half, bool first) {
           const uint32_t vo = (uint32_t)((item_v<QT>(j) % NS) * T::BYTES) >> 4;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 256 + DP * w, tmem + 128 * w + 8 * kk, dV + vo + kk * T::MN_STEP, idPV,
+          for (int k = 0; k < 4; ++k) {
+            const int kk = 4 * half + k;
+            mma_ts(tmem + 256 + DP * w, P0 + PW * w + 8 * kk, dV + vo + kk * T::MN_STEP, idPV,
                    (!first || kk > 0) ? 1u : 0u);
+          }
+        };
+        // waits for P of warpgroup w (its j-th use of the barriers) and multiplies
+        auto do_PV = [&](int w, int j, int use) -> bool {
+          if (!APART) {
+            if (!mbar_wait(&early[w], (uint32_t)(use & 1))) return false;
+            tc_fence_after();
+            issue_PV(w, j, 0, use == 0);
+          }
+          if (!mbar_wait(&p_ready[w], (uint32_t)(use & 1))) return false;
+          tc_fence_after();
+          if (APART) issue_PV(w, j, 0, use == 0);
+          issue_PV(w, j, 1, use == 0);
           mma_commit(&pv_done[w]);
+          return true;
         };
         if (QT == 2) {
           if (ok && (ok = full(item_k<QT>(0)))) {
@@ -239,6 +267,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n1 > 0) issue_S(1, 0);
             mma_commit(&kv_empty[item_k<QT>(0) % NS]);
           }
+        }
+        if (APART) {
+          // the warpgroups run half a tile apart: S0, then the other's product,
+          // S1, then this one's product
+          auto next_S = [&](int w, int j) -> bool {
+            if (!full(item_k<QT>(j + 1)) || !mbar_wait(&early[w], (uint32_t)(j & 1))) return false;
+            tc_fence_after();
+            issue_S(w, j + 1);
+            return true;
+          };
+          for (int j = 0; ok && j <= n; ++j) {
+            if (j + 1 < n0 && !(ok = next_S(0, j))) break;
+            if (j > 0) {
+              if (j - 1 < n1 && !(ok = full(item_v<QT>(j - 1)) && do_PV(1, j - 1, j - 1))) break;
+              mma_commit(&kv_empty[item_v<QT>(j - 1) % NS]);
+            }
+            if (j + 1 < n1 && !(ok = next_S(1, j))) break;
+            if (j + 1 < n) mma_commit(&kv_empty[item_k<QT>(j + 1) % NS]);
+            if (j < n0 && !(ok = full(item_v<QT>(j)) && do_PV(0, j, j))) break;
+            if (*abort_flag) ok = false;
+          }
+        } else if (QT == 2) {
           for (int j = 0; ok && j < n; ++j) {
             ok = full(item_v<QT>(j)) && (j + 1 >= n || full(item_k<QT>(j + 1)));
             if (!ok) break;
@@ -246,9 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 2; ++w) {
               const int nw = w ? n1 : n0;
               if (j >= nw) continue;
-              if (!(ok = mbar_wait(&p_ready[w], (uint32_t)(j & 1)))) break;
-              tc_fence_after();
-              issue_PV(w, j, j == 0);
+              if (!(ok = do_PV(w, j, j))) break;
               if (j + 1 < nw) issue_S(w, j + 1);
             }
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
@@ -264,10 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int j = 0; ok && j < n; ++j) {
             const int w = j & 1;
-            ok = full(item_v<QT>(j)) && mbar_wait(&p_ready[w], (uint32_t)((j >> 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            issue_PV(w, j, j < 2);
+            if (!(ok = full(item_v<QT>(j)) && do_PV(w, j, j >> 1))) break;
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
             if (j + 2 < n) {
               if (!(ok = full(item_k<QT>(j + 2)))) break;
@@ -295,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lb + 128 * w;
     const uint32_t tO = tmem + lb + 256 + DP * w;
+    const uint32_t tP = APART ? tmem + lb + 384 + 64 * w : tS;
     // the row's query and head
     int i, h;
     bool live;
@@ -318,6 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (!warp_live) {   // no row of this warp is stored
+        mbar_arrive(&early[w]);
+        // not ahead of the other warps' P of the tile before
+        if (APART && j > 0 && !warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
+          ok = false;
+          break;
+        }
         mbar_arrive(&p_ready[w]);
         continue;
       }
@@ -331,6 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld64(tS, a[0]);
       tmem_ld64(tS + 64, a[1]);
       tmem_wait_ld_dep128(a[0], a[1]);
+      if (APART) {
+        tc_fence_before();
+        mbar_arrive(&early[w]);
+      }
       if (masked) {
         mask_cols(a[0], 0, cl, ch);
         mask_cols(a[1], 64, cl, ch);
@@ -339,6 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       max_fold64(a[0], m4);
       max_fold64(a[1], m4);
       const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+      if (APART && j > 0) {   // the last product has read P (and O may be rescaled)
+        if (!warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+      }
       const bool move = (mx - mr) * A.c > kRescaleTau;
       if (warp_any(move)) {
         const float nm = move ? mx : mr;
@@ -346,12 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         mr = nm;
         if (j > 0) {
-          if (!warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
-            ok = false;
-            break;
+          if (!APART) {
+            if (!warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
+              ok = false;
+              break;
+            }
+            __syncwarp();
+            tc_fence_after();
           }
-          __syncwarp();
-          tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < DP / 32; ++k) {
             uint32_t o[32];
@@ -365,15 +431,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float neg = mr == -INFINITY ? 0.f : -mr * A.c;
       float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      // one block of straight code, so that the chunks' latencies overlap;
+      // masked tiles: the MUFU's exponential maps -inf to exactly 0
+      auto weights = [&](auto poly) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t pk[16];
-        const uint32_t* x = a[k >> 1] + 32 * (k & 1);
-        // masked tiles: the MUFU's exponential maps -inf to exactly 0
-        if (masked) exp_pack_pairs<16, 0>(x, A.c, neg, pk, s4);
-        else exp_pack_pairs<16, fwd_poly<DP>()>(x, A.c, neg, pk, s4);
-        tmem_st16(tS + 16 * k, pk);
-      }
+        for (int k = 0; k < 4; ++k) {
+          uint32_t pk[16];
+          exp_pack_pairs<16, decltype(poly)::value>(a[k >> 1] + 32 * (k & 1), A.c, neg, pk, s4);
+          tmem_st16(tP + 16 * k, pk);
+          if (!APART && k == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&early[w]);
+          }
+        }
+      };
+      if (masked) weights(std::integral_constant<int, 0>());
+      else weights(std::integral_constant<int, kFwdPoly>());
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&p_ready[w]);
