@@ -9,17 +9,27 @@ namespace flare {
 
 namespace {
 
-// The number of parts to cut each unit's `tiles` into on `slots` SMs:
-// minimises waves x (tiles per part + set-up of a CTA), plus the cost of
-// joining the parts when there is more than one; all in units of one tile.
-int choose_splits(int64_t units, int64_t tiles, int slots, double setup, double join) {
+// The number of parts to cut each of `units` pieces of work into, on `slots`
+// places: minimises an estimate of the time, in tiles, with `setup` for a
+// CTA's start and end, `join` for one more launch and `part` for writing and
+// reading back one part's sums.  Pieces of equal size run in waves.  With a
+// causal mask their sizes spread evenly up to `tiles`, longest first: the
+// places share the sum, and a piece at the end leaves some of them idle.
+int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double setup, double join,
+                  double part) {
   int best = 1;
   double best_cost = 1e300;
   const int64_t hi = imin64(tiles, imax64(1, 4LL * slots / imax64(units, 1)));
   for (int64_t s = 1; s <= hi; ++s) {
-    const int64_t waves = (units * s + slots - 1) / slots;
-    const double cost =
-        (double)waves * ((double)((tiles + s - 1) / s) + setup) + (s > 1 ? join : 0.0);
+    const double longest = (double)((tiles + s - 1) / s) + setup;
+    double cost;
+    if (causal) {
+      const double sum = (double)units * (0.5 * (double)tiles + (double)s * setup) / slots;
+      cost = fmax(longest, sum + 0.15 * longest);
+    } else {
+      cost = (double)((units * s + slots - 1) / slots) * longest;
+    }
+    if (s > 1) cost += join + part * (double)(units * s) / slots;
     if (cost < best_cost - 1e-9) {
       best_cost = cost;
       best = (int)s;
@@ -45,8 +55,15 @@ AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
   p.qblocks = (rows + p.rows - 1) / p.rows;
   p.units = d.B * (d.Hq / p.hpt) * p.qblocks;
   const int64_t ktiles = (d.Nk + tile - 1) / tile;
-  p.splits = tc ? choose_splits(p.units, ktiles, sms, p.qt == 2 ? 2.0 : 4.0, p.qt == 2 ? 4.0 : 8.0)
-                : choose_splits(p.units, ktiles, 2 * sms, 1.0, 2.0);
+  // one or a few tokens see about all keys
+  const bool triangle = d.causal && 2 * d.Nq > d.Nk;
+  // a part's rows x DP floats at an SM's share of the memory bandwidth (5500
+  // written and read back in a microsecond), against 2.0 us (two query tiles),
+  // 1.0 us (one) or 8 us for a tile (CUDA cores: two CTAs share an SM)
+  const double part =
+      (double)imin64(rows, p.rows) * attn_dp(d.D) / (tc ? 5500.0 * p.qt : 22000.0);
+  p.splits = tc ? choose_splits(p.units, ktiles, sms, triangle, p.qt == 2 ? 2.0 : 4.0, 3.0, part)
+                : choose_splits(p.units, ktiles, 2 * sms, triangle, 0.5, 0.5, part);
   return p;
 }
 
@@ -58,8 +75,13 @@ AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
   p.qtiles = (d.Nq + p.tile - 1) / p.tile;
   p.dkv_units = d.B * d.Hk * p.ktiles;
   p.dq_units = d.B * d.Hq * p.qtiles;
-  p.dkv_splits = choose_splits(p.dkv_units, d.G() * p.qtiles, sms, 2.0, 4.0);
-  p.dq_splits = choose_splits(p.dq_units, p.ktiles, sms, 2.0, 4.0);
+  const int slots = tc ? sms : 2 * sms;
+  const double setup = tc ? 2.0 : 0.5, join = tc ? 4.0 : 0.5;
+  const bool triangle = d.causal && d.Nq <= 2 * d.Nk && d.Nk <= 2 * d.Nq;
+  const double part = p.tile * attn_dp(d.D) / (tc ? 8000.0 : 22000.0);   // as the forward's
+  p.dkv_splits =
+      choose_splits(p.dkv_units, d.G() * p.qtiles, slots, triangle, setup, join, 2 * part);
+  p.dq_splits = choose_splits(p.dq_units, p.ktiles, slots, triangle, setup, join, part);
   return p;
 }
 
@@ -398,16 +420,18 @@ extern "C" {
 size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
                                  int64_t Nk, int64_t D, flare_dtype_t dt) {
   if (sizes(B, Hq, Hk, Nq, Nk, D, dt) != FLARE_OK) return 0;
-  AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, 0);
   const int sms = sm_count();
-  if (backward) return attn_ws_bwd(d, dt, attn_bwd_plan(d, dt, sms)).total;
-  // the plan of a call depends on whether its queries are broadcast over the
-  // heads: room for either
-  d.q.sh = 1;
-  const size_t own = attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
-  d.q.sh = 0;
-  const size_t rep = attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
-  return own > rep ? own : rep;
+  size_t most = 0;
+  // the plan of a call depends on its mask and on whether its queries are
+  // broadcast over the heads: room for any
+  for (int k = 0; k < 4; ++k) {
+    AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, k & 1);
+    d.q.sh = k >> 1;
+    const size_t need = backward ? attn_ws_bwd(d, dt, attn_bwd_plan(d, dt, sms)).total
+                                 : attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
+    most = need > most ? need : most;
+  }
+  return most;
 }
 
 flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void* Y,

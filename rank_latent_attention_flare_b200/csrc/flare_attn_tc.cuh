@@ -57,6 +57,17 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     tma_load_4d(dst + k * Tile<DP>::BLOCK, map, bar, 64 * k, row, h, b);
 }
 
+// One arrival for the whole warp, once all its lanes are here.  Predicated,
+// so that the warp stays converged for the collective instructions after it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(threadIdx.x & 31u)
+      : "memory");
+}
+
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return (uint8_t*)(((uintptr_t)p + 1023) & ~(uintptr_t)1023);
 }

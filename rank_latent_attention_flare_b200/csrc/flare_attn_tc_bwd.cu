@@ -43,32 +43,26 @@ constexpr int kBThreads = 640;
 constexpr int kBWarpTma = 16, kBWarpMma = 17, kBWarpAux = 18;
 constexpr int kCols = 32;
 
-// 2^(c a + n) for a lane's columns, in place, n[] per column or one for all:
+// 2^(c a + n) for a lane's columns, in place, n per column or one for all:
 // probabilities in float32.
 template <bool COLS, int POLY>
-__device__ __forceinline__ void exp_cols(uint32_t (&a)[kCols], float c, float n, const float* cols) {
+__device__ __forceinline__ void exp_cols(uint32_t (&a)[kCols], float c, float n,
+                                         const float (&cols)[COLS ? kCols : 1]) {
   const uint64_t c2 = f32x2(c, c);
 #pragma unroll
-  for (int t = 0; t < kCols; t += 4) {
-    float4 v;
-    if (COLS) v = *reinterpret_cast<const float4*>(cols + t);
-    else v = make_float4(n, n, n, n);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = t + 2 * h;
-      const uint64_t x = fma_f32x2(f32x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), c2,
-                                   h ? f32x2(v.z, v.w) : f32x2(v.x, v.y));
-      float p0, p1;
-      if (POLY > 0 && (i / 2) % (POLY > 0 ? POLY : 1) == POLY - 1) {
-        exp2_fma_pair(x, p0, p1);
-      } else {
-        split_f32x2(x, p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-      }
-      a[i] = __float_as_uint(p0);
-      a[i + 1] = __float_as_uint(p1);
+  for (int i = 0; i < kCols; i += 2) {
+    const uint64_t x = fma_f32x2(f32x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), c2,
+                                 COLS ? f32x2(cols[COLS ? i : 0], cols[COLS ? i + 1 : 0]) : f32x2(n, n));
+    float p0, p1;
+    if (POLY > 0 && (i / 2) % (POLY > 0 ? POLY : 1) == POLY - 1) {
+      exp2_fma_pair(x, p0, p1);
+    } else {
+      split_f32x2(x, p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
     }
+    a[i] = __float_as_uint(p0);
+    a[i + 1] = __float_as_uint(p1);
   }
 }
 
@@ -152,7 +146,7 @@ struct DkvLayout {
   static constexpr int RING_OFF = 2 * T::BYTES;
   static constexpr int NL_OFF = RING_OFF + SLOTS * T::BYTES;       // [NB][nl 128, delta 128]
   static constexpr int BAR_OFF = NL_OFF + NB * 1024;
-  static constexpr int NBARS = 2 * SLOTS + 1 + 2 * NB + 4 + 1;
+  static constexpr int NBARS = 2 * SLOTS + 1 + 2 * NB + 6 + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int BYTES = MISC_OFF + 16;
 };
@@ -175,14 +169,19 @@ __global__ void __launch_bounds__(kBThreads, 1)
   uint64_t* kv_full = bars + 2 * NS;
   uint64_t* nl_full = kv_full + 1;     // [NB]
   uint64_t* nl_empty = nl_full + NB;   // [NB]
-  uint64_t* s_full = nl_empty + NB;
-  uint64_t* p_ready = s_full + 1;
-  uint64_t* dp_full = s_full + 2;
-  uint64_t* ds_ready = s_full + 3;
-  uint64_t* done = s_full + 4;
+  uint64_t* s_full = nl_empty + NB;    // [buffer of S]
+  // [buffer of S]: with two of them a fast warp may be one tile ahead of a
+  // slow one, and its arrival must not count for the tile before
+  uint64_t* p_ready = s_full + 2;
+  uint64_t* dp_full = s_full + 4;
+  uint64_t* ds_ready = s_full + 5;
+  uint64_t* done = s_full + 6;
   uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
   volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
-  constexpr uint32_t TS = 0, TP = 128, TK = 256, TV = 256 + DP;
+  // S has two buffers where TMEM has room (SB = 2): S of tile j + 2 then
+  // follows dV of tile j, and the softmax never waits for it
+  constexpr int SB = DP <= 64 ? 2 : 1;
+  constexpr uint32_t TP = 128 * SB, TK = TP + 128, TV = TK + DP;   // S at 0
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -216,13 +215,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * NS + 1; ++s) mbar_init(&bars[s], 1);
     for (int s = 0; s < NB; ++s) {
-      mbar_init(&nl_full[s], 32);
-      mbar_init(&nl_empty[s], 512);
+      mbar_init(&nl_full[s], 1);
+      mbar_init(&nl_empty[s], 16);
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_ready, 512);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_ready[s], 16);
+    }
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 512);
+    mbar_init(ds_ready, 16);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -294,20 +295,27 @@ __global__ void __launch_bounds__(kBThreads, 1)
                  (!start || kk > 0) ? 1u : 0u);
         mma_commit(&empty[it % NS]);
       };
+      auto issue_S = [&](int j) {
+        issue_nt(128 * (j % SB), dK, 2 * j, &s_full[j % SB]);
+      };
       bool ok = mbar_wait(kv_full, 0) && landed(0) && landed(1);
       if (ok) {
         tc_fence_after();
-        issue_nt(TS, dK, 0, s_full);
+        issue_S(0);
         issue_nt(TP, dV, 1, dp_full);
       }
-      for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = mbar_wait(p_ready, (uint32_t)(j & 1)))) break;
+      if (SB == 2 && ok && n > 1 && (ok = landed(2))) {
         tc_fence_after();
-        issue_nn(TV, TS, 2 * j + 1, j == 0);
-        if (j + 1 < n) {
-          if (!(ok = landed(2 * j + 2))) break;
+        issue_S(1);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = mbar_wait(&p_ready[j % SB], (uint32_t)((j / SB) & 1)))) break;
+        tc_fence_after();
+        issue_nn(TV, 128 * (j % SB), 2 * j + 1, j == 0);
+        if (j + SB < n) {
+          if (!(ok = landed(2 * (j + SB)))) break;
           tc_fence_after();
-          issue_nt(TS, dK, 2 * j + 2, s_full);
+          issue_S(j + SB);
         }
         if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
         tc_fence_after();
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         dst[col] = own ? A.nl[base + q] : -INFINITY;
         dst[128 + col] = own ? A.delta[base + q] : 0.f;
       }
-      mbar_arrive(&nl_full[s]);
+      warp_arrive(&nl_full[s]);
     }
     if (!ok) {
       record_error(A.err, kErrAttnDkvRowWait);
@@ -358,17 +366,29 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;   // TMEM lane: key krow0 + r
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lb + TS + kCols * w, tP = tmem + lb + TP + kCols * w;
+    const uint32_t tP = tmem + lb + TP + kCols * w;
     bool ok = true;
+    int t = first + (n > 0 ? lo % per : 0);   // the query tile
     for (int j = 0; j < n; ++j) {
       const int s = j % NB;
-      const int x = lo + j, t = first + x % per;
+      const uint32_t tS = tmem + lb + 128 * (j % SB) + kCols * w;
       const int row0 = tile_row0(t, kAttnTile, sq.ql);
+      if (++t == first + per) t = first;
       // columns below cl do not see this lane's key
       const int cl = sq.causal ? krow0 + r - sq.off - row0 - kCols * w : -1;
       const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
-      if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((j / NB) & 1)) &&
-                    mbar_wait(s_full, (uint32_t)(j & 1)))) {
+      if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((j / NB) & 1)))) {
+        ok = false;
+        break;
+      }
+      float nv[kCols];   // read ahead of the wait for S
+#pragma unroll
+      for (int x = 0; x < kCols; x += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(nl + x);
+        nv[x] = v.x, nv[x + 1] = v.y, nv[x + 2] = v.z, nv[x + 3] = v.w;
+      }
+      const bool gone = nl[lane] == -INFINITY;
+      if (!warp_all(mbar_wait(&s_full[j % SB], (uint32_t)((j / SB) & 1)))) {
         ok = false;
         break;
       }
@@ -379,17 +399,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tmem_wait_ld_dep(p);
       // a tile with masked columns or rows without weight keeps to the MUFU,
       // whose exponential of -inf is 0
-      const bool gone = nl[lane] == -INFINITY;
       if (warp_any(cl > 0 || gone)) {
         mask_cols(p, 0, cl, kCols - 1);
-        exp_cols<true, 0>(p, A.c, 0.f, nl);
+        exp_cols<true, 0>(p, A.c, 0.f, nv);
       } else {
-        exp_cols<true, kBwdPoly>(p, A.c, 0.f, nl);
+        exp_cols<true, kBwdPoly>(p, A.c, 0.f, nv);
       }
       store_bf16_tmem(tS, p);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(p_ready);
+      warp_arrive(&p_ready[j % SB]);
       if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
         ok = false;
         break;
@@ -400,11 +419,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tmem_ld32(tP, g);
       tmem_wait_ld_dep(g);
       ds_cols<true>(g, p, 0.f, nl + 128);
-      mbar_arrive(&nl_empty[s]);
+      warp_arrive(&nl_empty[s]);
       store_bf16_tmem(tP, g);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(ds_ready);
+      warp_arrive(ds_ready);
     }
     if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
     if (!ok) {
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 512);
+    mbar_init(ds_ready, 16);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -628,6 +647,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const float nl = live && i < sq.ql ? A.nl[row] : -INFINITY;
     const float delta = live && i < sq.ql ? A.delta[row] : 0.f;
     const bool gone = nl == -INFINITY;
+    const float none[1] = {0.f};
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int t = lo + j;
@@ -645,9 +665,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tmem_wait_ld_dep(p);
       if (warp_any(cl > 0 || ch < kCols - 1 || gone)) {
         mask_cols(p, 0, cl, ch);
-        exp_cols<false, 0>(p, A.c, nl, nullptr);
+        exp_cols<false, 0>(p, A.c, nl, none);
       } else {
-        exp_cols<false, kBwdPoly>(p, A.c, nl, nullptr);
+        exp_cols<false, kBwdPoly>(p, A.c, nl, none);
       }
       if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
         ok = false;
@@ -662,7 +682,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       store_bf16_tmem(tP, g);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(ds_ready);
+      warp_arrive(ds_ready);
     }
     if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
     if (!ok) {

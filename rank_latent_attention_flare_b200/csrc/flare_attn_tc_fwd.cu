@@ -146,9 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_ready[w], 128);
+      mbar_init(&p_ready[w], 4);
       mbar_init(&pv_done[w], 1);
-      mbar_init(&early[w], 128);
+      mbar_init(&early[w], 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -364,13 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (!warp_live) {   // no row of this warp is stored
-        mbar_arrive(&early[w]);
+        warp_arrive(&early[w]);
         // not ahead of the other warps' P of the tile before
         if (APART && j > 0 && !warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
           ok = false;
           break;
         }
-        mbar_arrive(&p_ready[w]);
+        warp_arrive(&p_ready[w]);
         continue;
       }
       __syncwarp();
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld_dep128(a[0], a[1]);
       if (APART) {
         tc_fence_before();
-        mbar_arrive(&early[w]);
+        warp_arrive(&early[w]);
       }
       if (masked) {
         mask_cols(a[0], 0, cl, ch);
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!APART && k == 1) {
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&early[w]);
+            warp_arrive(&early[w]);
           }
         }
       };
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else weights(std::integral_constant<int, kFwdPoly>());
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_ready[w]);
+      warp_arrive(&p_ready[w]);
       l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
     }
     if (ok && nw > 0 && !warp_all(mbar_wait(&pv_done[w], (uint32_t)((nw - 1) & 1)))) ok = false;

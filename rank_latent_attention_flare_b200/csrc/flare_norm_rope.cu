@@ -12,21 +12,32 @@
 // Both kernels are bound by memory: one pass, a row held in the registers of
 // LPG lanes (16 bytes each, so D = 128 in bf16 takes 16 lanes), all sums in
 // float32, one rounding at the end.  A pair's other half sits in another lane
-// when pairs are (i, i + R / 2): it comes by a shuffle.  A group of lanes
-// takes one token and up to kHeads heads, so that the token's angles and the
-// weights are loaded once for them and four rows are in flight per lane.
+// when pairs are (i, i + R / 2): its raw 16 bytes come by a shuffle, and the
+// weights are folded into the angles, y = r (x (w cos) + x' (w' sin)), so that
+// a row costs about six instructions for every element pair (packed float32
+// arithmetic); with more of them the kernel is bound by issue slots.  A group
+// of lanes takes one token and up to 8 heads of it, so that the coefficients
+// are built once for them.
 #include "flare_attn.cuh"
+#include "tc_primitives.cuh"
 
 namespace flare {
 namespace {
 
+using tc::add_f32x2;
+using tc::f32x2;
+using tc::fma_f32x2;
+using tc::mul_f32x2;
+using tc::split_f32x2;
+
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // rows in flight per group
+constexpr int kBwdPerSm = 3;   // resident CTAs of the backward
 
 struct NormRopeArgs {
   int Hq, Hk, N, D, R, interleaved;
   int qchunks, kchunks, heads;   // units per token, heads per unit
   int h_inner;                   // units of a token are neighbours (else tokens of a chunk)
+  int qblocks, kblocks;          // backward: CTAs for q and for k
   int64_t tokens, units;         // tokens = B N
   int64_t tab_sb;                // batch stride of cos / sin
   float eps;
@@ -34,127 +45,134 @@ struct NormRopeArgs {
   const void *q, *k, *wq, *wk, *dqo, *dko;
   void *qo, *ko, *dq, *dk, *dwq, *dwk;
   Tok tq, tk, tqo, tko, tdq, tdk;   // tqo, tko: of the outputs or their gradients
-  float* part;                      // backward: [blocks][2][128] weight gradients
+  float* part;                      // backward: [block][128] weight gradients
 };
 
+// The 16 bytes of a lane as pairs of float32.
 template <typename T>
 struct Vec {
-  static constexpr int V = 16 / sizeof(T);
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[V]) {
+  static constexpr int V = 16 / sizeof(T), P = V / 2;
+  static __device__ __forceinline__ void unpack(const uint4& u, uint64_t (&f)[P]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (sizeof(T) == 4) {
-        f[k] = __uint_as_float(w[k]);
-      } else {
-        f[2 * k] = __uint_as_float(w[k] << 16);
-        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
+    for (int k = 0; k < P; ++k) {
+      if constexpr (sizeof(T) == 4)
+        f[k] = f32x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+      else
+        f[k] = f32x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
     }
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[V]) {
+  static __device__ __forceinline__ uint4 pack(const uint64_t (&f)[P]) {
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < P; ++k) {
+      float a, b;
+      split_f32x2(f[k], a, b);
       if constexpr (sizeof(T) == 4) {
-        w[k] = __float_as_uint(f[k]);
+        w[2 * k] = __float_as_uint(a);
+        w[2 * k + 1] = __float_as_uint(b);
       } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        w[k] = tc::pack_bf16(a, b);
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // the elements at column d of a [D] vector (ones without one)
+  static __device__ __forceinline__ void weights(const void* w, int d, int D, uint64_t (&f)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) f[k] = f32x2(1.f, 1.f);
+    if (w != nullptr && d < D) unpack(__ldg((const uint4*)((const T*)w + d)), f);
+  }
 };
 
-// What a unit of work is: token (b, n) and heads [h0, h0 + cnt) of q or k.
-struct Unit {
-  int64_t b;
-  int n, h0, cnt;
-  bool k;
-};
-__device__ __forceinline__ Unit unit_of(const NormRopeArgs& A, int64_t u) {
-  const int chunks = A.qchunks + A.kchunks;
-  int64_t tok;
-  int c;
-  if (A.h_inner) {
-    tok = u / chunks;
-    c = (int)(u % chunks);
-  } else {   // neighbouring groups: neighbouring tokens of one chunk
-    const int64_t per = (int64_t)chunks * A.N;
-    const int64_t b = u / per;
-    const int64_t x = u % per;
-    c = (int)(x / A.N);
-    tok = b * A.N + x % A.N;
-  }
-  Unit r;
-  r.b = tok / A.N;
-  r.n = (int)(tok % A.N);
-  r.k = c >= A.qchunks;
-  r.h0 = (r.k ? c - A.qchunks : c) * A.heads;
-  r.cnt = min(A.heads, (r.k ? A.Hk : A.Hq) - r.h0);
-  return r;
+__device__ __forceinline__ uint64_t swap_f32x2(uint64_t v) {
+  float a, b;
+  split_f32x2(v, a, b);
+  return f32x2(b, a);
+}
+__device__ __forceinline__ float sum_f32x2(uint64_t v) {
+  float a, b;
+  split_f32x2(v, a, b);
+  return a + b;
 }
 
-// The angles of a lane's elements, and how it finds its pairs' other halves.
-template <int V>
+// unit u of `chunks` chunks per token (32-bit divisions where they reach)
+__device__ __forceinline__ void unit_of(const NormRopeArgs& A, int64_t u, int chunks, int64_t& b,
+                                        int& n, int& c) {
+  if (A.units <= 0x7fffffffLL) {
+    const unsigned v = (unsigned)u, N = (unsigned)A.N, C = (unsigned)chunks;
+    if (A.h_inner) {
+      c = (int)(v % C);
+      b = (int64_t)(v / C / N);
+      n = (int)(v / C % N);
+    } else {   // neighbouring groups: neighbouring tokens of one chunk
+      n = (int)(v % N);
+      c = (int)(v / N % C);
+      b = (int64_t)(v / N / C);
+    }
+  } else if (A.h_inner) {
+    c = (int)(u % chunks);
+    b = u / chunks / A.N;
+    n = (int)(u / chunks % A.N);
+  } else {
+    n = (int)(u % A.N);
+    c = (int)(u / A.N % chunks);
+    b = u / A.N / chunks;
+  }
+}
+
+// A lane's cosines, and sines with the sign of the other half's term in the
+// rotation; where the other half is.
+template <typename T>
 struct Angles {
-  float c[V], s[V];   // s carries the sign of the other half's term
-  int src;            // lane that holds the other halves
-  __device__ __forceinline__ void load(const NormRopeArgs& A, const Unit& u, int sub, int lane) {
-    const int d = sub * V;
-    src = lane;
+  static constexpr int P = Vec<T>::P;
+  uint64_t c[P], s[P];
+  int other;   // column of the other half (split pairs)
+  __device__ __forceinline__ void load(const NormRopeArgs& A, int64_t b, int n, int d) {
+    other = d;
 #pragma unroll
-    for (int e = 0; e < V; ++e) c[e] = 1.f, s[e] = 0.f;
+    for (int k = 0; k < P; ++k) c[k] = f32x2(1.f, 1.f), s[k] = 0;
     if (d >= A.R) return;
     const int half = A.R / 2;
-    const int64_t row = u.b * A.tab_sb + (int64_t)u.n * half;
+    const int64_t row = b * A.tab_sb + (int64_t)n * half;
     if (A.interleaved) {
 #pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float cc = __ldg(A.cos + row + (d + e) / 2), ss = __ldg(A.sin + row + (d + e) / 2);
-        c[e] = c[e + 1] = cc;
-        s[e] = -ss;
-        s[e + 1] = ss;
+      for (int k = 0; k < P; ++k) {
+        const float cc = __ldg(A.cos + row + d / 2 + k), ss = __ldg(A.sin + row + d / 2 + k);
+        c[k] = f32x2(cc, cc);
+        s[k] = f32x2(-ss, ss);
       }
-    } else {
-      const bool second = d >= half;
-      const int64_t at = row + (second ? d - half : d);
-      src = second ? lane - half / V : lane + half / V;
-#pragma unroll
-      for (int e = 0; e < V; e += 4) {
-        const float4 cc = __ldg((const float4*)(A.cos + at + e));
-        const float4 ss = __ldg((const float4*)(A.sin + at + e));
-        c[e] = cc.x, c[e + 1] = cc.y, c[e + 2] = cc.z, c[e + 3] = cc.w;
-        s[e] = ss.x, s[e + 1] = ss.y, s[e + 2] = ss.z, s[e + 3] = ss.w;
-      }
-      if (!second)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[e] = -s[e];
+      return;
     }
-  }
-  // y = rotation(u), or its inverse (SIGN = -1).  Whole-warp call.
-  template <int SIGN>
-  __device__ __forceinline__ void rotate(const float (&u)[V], float (&y)[V], int interleaved) const {
-    float o[V];
-    if (interleaved) {
+    const bool second = d >= half;
+    other = second ? d - half : d + half;
+    const float* pc = A.cos + row + (second ? d - half : d);
+    const float* ps = A.sin + row + (second ? d - half : d);
+    const float sign = second ? 1.f : -1.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = u[e ^ 1];
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = __shfl_sync(0xffffffffu, u[e], src);
+    for (int k = 0; k < P; k += 2) {
+      const float4 cc = __ldg((const float4*)(pc + 2 * k)), ss = __ldg((const float4*)(ps + 2 * k));
+      c[k] = f32x2(cc.x, cc.y), c[k + 1] = f32x2(cc.z, cc.w);
+      s[k] = f32x2(sign * ss.x, sign * ss.y), s[k + 1] = f32x2(sign * ss.z, sign * ss.w);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = fmaf(o[e], SIGN * s[e], u[e] * c[e]);
   }
 };
 
-template <int V, typename T>
-__device__ __forceinline__ void load_w(const void* w, int sub, int D, float (&f)[V]) {
+// The other halves of a lane's elements.  Whole-warp call.
+template <typename T>
+__device__ __forceinline__ void others(const uint4& raw, const uint64_t (&x)[Vec<T>::P],
+                                       bool interleaved, int src, uint64_t (&o)[Vec<T>::P]) {
+  if (interleaved) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = 1.f;
-  if (w != nullptr && sub * V < D)
-    Vec<T>::unpack(__ldg((const uint4*)((const T*)w + sub * V)), f);
+    for (int k = 0; k < Vec<T>::P; ++k) o[k] = swap_f32x2(x[k]);
+  } else {
+    uint4 t;
+    t.x = __shfl_sync(0xffffffffu, raw.x, src);
+    t.y = __shfl_sync(0xffffffffu, raw.y, src);
+    t.z = __shfl_sync(0xffffffffu, raw.z, src);
+    t.w = __shfl_sync(0xffffffffu, raw.w, src);
+    Vec<T>::unpack(t, o);
+  }
 }
 
 template <int LPG>
@@ -165,133 +183,157 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 template <typename T, int LPG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     norm_rope_fwd_kernel(const __grid_constant__ NormRopeArgs A) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = Vec<T>::V;
-  const int lane = threadIdx.x & 31, sub = threadIdx.x % LPG;
+  constexpr int V = Vec<T>::V, P = Vec<T>::P, U = 4;   // U rows in flight per lane
+  const int lane = threadIdx.x & 31, sub = threadIdx.x % LPG, d = sub * V;
   const int64_t id = (int64_t)blockIdx.x * (kThreads / LPG) + threadIdx.x / LPG;
   const bool on = id < A.units;            // every lane stays for the shuffles
-  const Unit u = unit_of(A, on ? id : 0);
-  const bool in = on && sub * V < A.D;
-  Angles<V> ang;
-  ang.load(A, u, sub, lane);
-  float w[V];
-  load_w<V, T>(u.k ? A.wk : A.wq, sub, A.D, w);
-  const Tok ti = u.k ? A.tk : A.tq, to = u.k ? A.tko : A.tqo;
-  const T* x = (const T*)(u.k ? A.k : A.q) + u.b * ti.sb + u.n * ti.sn + sub * V;
-  T* y = (T*)(u.k ? A.ko : A.qo) + u.b * to.sb + u.n * to.sn + sub * V;
-  const float inv = 1.f / A.D;
-  for (int h = 0; h < A.heads; h += kUnroll) {
-    uint4 raw[kUnroll];
+  int64_t b;
+  int n, ch;
+  unit_of(A, on ? id : 0, A.qchunks + A.kchunks, b, n, ch);
+  const bool isk = ch >= A.qchunks;
+  const int h0 = (isk ? ch - A.qchunks : ch) * A.heads;
+  const int cnt = on && d < A.D ? min(A.heads, (isk ? A.Hk : A.Hq) - h0) : 0;
+  const Tok ti = isk ? A.tk : A.tq, to = isk ? A.tko : A.tqo;
+  const T* x = (const T*)(isk ? A.k : A.q) + b * ti.sb + n * ti.sn + h0 * ti.sh + d;
+  T* y = (T*)(isk ? A.ko : A.qo) + b * to.sb + n * to.sn + h0 * to.sh + d;
+  const void* w = isk ? A.wk : A.wq;
+  // y = r (x ca + x' cb)
+  uint64_t ca[P], cb[P];
+  int src;
+  {
+    Angles<T> ang;
+    ang.load(A, b, n, d);
+    src = lane + (ang.other - d) / V;
+    uint64_t wx[P], wo[P];
+    Vec<T>::weights(w, d, A.D, wx);
+    Vec<T>::weights(w, ang.other, A.D, wo);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+    for (int k = 0; k < P; ++k) {
+      ca[k] = mul_f32x2(ang.c[k], wx[k]);
+      cb[k] = mul_f32x2(ang.s[k], A.interleaved ? swap_f32x2(wx[k]) : wo[k]);
+    }
+  }
+  const float inv = 1.f / A.D;
+  for (int h = 0; h < A.heads; h += U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
       raw[j] = make_uint4(0, 0, 0, 0);
-      if (in && h + j < u.cnt)
-        raw[j] = *reinterpret_cast<const uint4*>(x + (u.h0 + h + j) * ti.sh);
+      if (h + j < cnt) raw[j] = *reinterpret_cast<const uint4*>(x + (h + j) * ti.sh);
     }
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      float f[V], o[V], ss = 0.f;
+    for (int j = 0; j < U; ++j) {
+      uint64_t f[P], o[P], ss = 0;
       Vec<T>::unpack(raw[j], f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(f[e], f[e], ss);
-      const float r = rsqrtf(fmaf(group_sum<LPG>(ss), inv, A.eps));
+      for (int k = 0; k < P; ++k) ss = fma_f32x2(f[k], f[k], ss);
+      const float r = rsqrtf(fmaf(group_sum<LPG>(sum_f32x2(ss)), inv, A.eps));
+      others<T>(raw[j], f, A.interleaved, src, o);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] *= w[e] * r;
-      ang.template rotate<1>(f, o, A.interleaved);
-      if (in && h + j < u.cnt)
-        *reinterpret_cast<uint4*>(y + (u.h0 + h + j) * to.sh) = Vec<T>::pack(o);
+      for (int k = 0; k < P; ++k)
+        f[k] = mul_f32x2(fma_f32x2(o[k], cb[k], mul_f32x2(f[k], ca[k])), f32x2(r, r));
+      if (h + j < cnt) *reinterpret_cast<uint4*>(y + (h + j) * to.sh) = Vec<T>::pack(f);
     }
   }
 }
 
-// A fixed number of CTAs take the units in turn, so that the weight gradients
-// stay in registers until the end; a CTA's groups are added in a fixed order.
+// The CTAs that reside at once take the units in turn, those of q and those
+// of k apart, so that the weight gradient stays in registers until the end; a
+// CTA's groups are added in a fixed order.
 template <typename T, int LPG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdPerSm)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs A) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = Vec<T>::V, GROUPS = kThreads / LPG;
+  constexpr int V = Vec<T>::V, P = Vec<T>::P, U = 2, GROUPS = kThreads / LPG;
   __shared__ float red[GROUPS][LPG * V + 4];
   const int lane = threadIdx.x & 31, sub = threadIdx.x % LPG, group = threadIdx.x / LPG;
+  const int d = sub * V;
+  const bool isk = (int)blockIdx.x >= A.qblocks;
+  const int block = (int)blockIdx.x - (isk ? A.qblocks : 0), blocks = isk ? A.kblocks : A.qblocks;
+  const int chunks = isk ? A.kchunks : A.qchunks, H = isk ? A.Hk : A.Hq;
+  const int64_t units = A.tokens * chunks;
+  const Tok ti = isk ? A.tk : A.tq, tg = isk ? A.tko : A.tqo, to = isk ? A.tdk : A.tdq;
+  uint64_t w[P], acc[P];
+  Vec<T>::weights(isk ? A.wk : A.wq, d, A.D, w);
+#pragma unroll
+  for (int k = 0; k < P; ++k) acc[k] = 0;
   const float inv = 1.f / A.D;
-  float dw[2][V] = {};
-  for (int64_t base = (int64_t)blockIdx.x * GROUPS; base < A.units;
-       base += (int64_t)gridDim.x * GROUPS) {
+  for (int64_t base = (int64_t)block * GROUPS; base < units; base += (int64_t)blocks * GROUPS) {
     const int64_t id = base + group;
-    const bool on = id < A.units;
-    const Unit u = unit_of(A, on ? id : 0);
-    const bool in = on && sub * V < A.D;
-    Angles<V> ang;
-    ang.load(A, u, sub, lane);
-    float w[V], acc[V] = {};
-    load_w<V, T>(u.k ? A.wk : A.wq, sub, A.D, w);
-    const Tok ti = u.k ? A.tk : A.tq, tg = u.k ? A.tko : A.tqo, to = u.k ? A.tdk : A.tdq;
-    const T* x = (const T*)(u.k ? A.k : A.q) + u.b * ti.sb + u.n * ti.sn + sub * V;
-    const T* g = (const T*)(u.k ? A.dko : A.dqo) + u.b * tg.sb + u.n * tg.sn + sub * V;
-    T* dx = (T*)(u.k ? A.dk : A.dq) + u.b * to.sb + u.n * to.sn + sub * V;
-    for (int h = 0; h < A.heads; h += kUnroll) {
-      uint4 rx[kUnroll], rg[kUnroll];
+    const bool on = id < units;
+    int64_t b;
+    int n, ch;
+    unit_of(A, on ? id : 0, chunks, b, n, ch);
+    const int h0 = ch * A.heads;
+    const int cnt = on && d < A.D ? min(A.heads, H - h0) : 0;
+    Angles<T> ang;
+    ang.load(A, b, n, d);
+    const int src = lane + (ang.other - d) / V;
+    const T* x = (const T*)(isk ? A.k : A.q) + b * ti.sb + n * ti.sn + h0 * ti.sh + d;
+    const T* g = (const T*)(isk ? A.dko : A.dqo) + b * tg.sb + n * tg.sn + h0 * tg.sh + d;
+    T* dx = (T*)(isk ? A.dk : A.dq) + b * to.sb + n * to.sn + h0 * to.sh + d;
+    for (int h = 0; h < A.heads; h += U) {
+      uint4 rx[U], rg[U];
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
+      for (int j = 0; j < U; ++j) {
         rx[j] = rg[j] = make_uint4(0, 0, 0, 0);
-        if (in && h + j < u.cnt) {
-          rx[j] = *reinterpret_cast<const uint4*>(x + (u.h0 + h + j) * ti.sh);
-          rg[j] = *reinterpret_cast<const uint4*>(g + (u.h0 + h + j) * tg.sh);
+        if (h + j < cnt) {
+          rx[j] = *reinterpret_cast<const uint4*>(x + (h + j) * ti.sh);
+          rg[j] = *reinterpret_cast<const uint4*>(g + (h + j) * tg.sh);
         }
       }
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        float f[V], d[V], du[V], ss = 0.f, gx = 0.f;
+      for (int j = 0; j < U; ++j) {
+        uint64_t f[P], e[P], o[P], ss = 0, gx = 0;
         Vec<T>::unpack(rx[j], f);
-        Vec<T>::unpack(rg[j], d);
-        ang.template rotate<-1>(d, du, A.interleaved);
+        Vec<T>::unpack(rg[j], e);
+        others<T>(rg[j], e, A.interleaved, src, o);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          d[e] = du[e] * w[e];
-          ss = fmaf(f[e], f[e], ss);
-          gx = fmaf(d[e], f[e], gx);
+        for (int k = 0; k < P; ++k) {
+          // du: the inverse rotation has the other sign of the sine
+          o[k] = fma_f32x2(o[k], ang.s[k] ^ 0x8000000080000000ull, mul_f32x2(e[k], ang.c[k]));
+          e[k] = mul_f32x2(o[k], w[k]);
+          ss = fma_f32x2(f[k], f[k], ss);
+          gx = fma_f32x2(e[k], f[k], gx);
         }
-        const float r = rsqrtf(fmaf(group_sum<LPG>(ss), inv, A.eps));
-        const float m = group_sum<LPG>(gx) * inv * r * r;
+        const float r = rsqrtf(fmaf(group_sum<LPG>(sum_f32x2(ss)), inv, A.eps));
+        const float m = -group_sum<LPG>(sum_f32x2(gx)) * inv * r * r * r;
+        const uint64_t r2 = f32x2(r, r), m2 = f32x2(m, m);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          acc[e] = fmaf(du[e], f[e] * r, acc[e]);
-          d[e] = r * fmaf(-f[e], m, d[e]);
+        for (int k = 0; k < P; ++k) {
+          acc[k] = fma_f32x2(o[k], mul_f32x2(f[k], r2), acc[k]);
+          e[k] = fma_f32x2(f[k], m2, mul_f32x2(e[k], r2));
         }
-        if (in && h + j < u.cnt)
-          *reinterpret_cast<uint4*>(dx + (u.h0 + h + j) * to.sh) = Vec<T>::pack(d);
+        if (h + j < cnt) *reinterpret_cast<uint4*>(dx + (h + j) * to.sh) = Vec<T>::pack(e);
       }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      dw[0][e] += u.k ? 0.f : acc[e];
-      dw[1][e] += u.k ? acc[e] : 0.f;
     }
   }
+  if ((isk ? A.dwk : A.dwq) == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if ((k ? A.dwk : A.dwq) == nullptr) continue;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[group][sub * V + e] = dw[k][e];
-    __syncthreads();
-    if (threadIdx.x < A.D) {
-      float s = 0.f;
-      for (int gq = 0; gq < GROUPS; ++gq) s += red[gq][threadIdx.x];
-      A.part[((int64_t)blockIdx.x * 2 + k) * 128 + threadIdx.x] = s;
-    }
+  for (int k = 0; k < P; ++k) {
+    float a, c;
+    split_f32x2(acc[k], a, c);
+    red[group][d + 2 * k] = a;
+    red[group][d + 2 * k + 1] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x < A.D) {
+    float s = 0.f;
+    for (int q = 0; q < GROUPS; ++q) s += red[q][threadIdx.x];
+    A.part[(int64_t)blockIdx.x * 128 + threadIdx.x] = s;
   }
 }
 
 // The CTAs' weight gradients, added in a fixed order: 32 columns per CTA, a
 // warp per eighth of the records.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* part, int n, int D, T* dwq,
-                                                           T* dwk) {
+__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* part, int nq, int nk, int D,
+                                                           T* dwq, T* dwk) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[8][32];
@@ -299,9 +341,12 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* part, in
   const int k = blockIdx.x / 4, col = (blockIdx.x % 4) * 32 + lane;
   T* out = k ? dwk : dwq;
   if (out == nullptr) return;
+  const int lo = k ? nq : 0, hi = k ? nq + nk : nq;
   float s = 0.f;
-  if (col < D)
-    for (int i = warp; i < n; i += 8) s += part[((int64_t)i * 2 + k) * 128 + col];
+  if (col < D) {
+#pragma unroll 8
+    for (int i = lo + warp; i < hi; i += 8) s += part[(int64_t)i * 128 + col];
+  }
   red[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || col >= D) return;
@@ -317,21 +362,30 @@ int lanes_per_row(int64_t D, flare_dtype_t dt) {
   return lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
 }
 
-// CTAs of the backward: a multiple of the SMs, never more than the units.
-int64_t bwd_blocks(int64_t units, int lpg) {
-  const int64_t need = (units * lpg + kThreads - 1) / kThreads;
-  return imin64(need, 4LL * sm_count());
-}
-
-constexpr int64_t kPartBytes = 2 * 128 * 4;
-
-void cut(NormRopeArgs& a, int64_t B) {
-  a.heads = kUnroll;
-  a.qchunks = (a.Hq + a.heads - 1) / a.heads;
-  a.kchunks = (a.Hk + a.heads - 1) / a.heads;
+// Heads per unit: 8, or fewer where that leaves SMs without a CTA (a single
+// token of 32 requests: 1).
+void cut(NormRopeArgs& a, int64_t B, int lpg) {
+  const int64_t per = kThreads / lpg, want = sm_count() * per;
   a.tokens = B * a.N;
-  a.units = a.tokens * (a.qchunks + a.kchunks);
+  for (a.heads = 8;; a.heads /= 2) {
+    a.qchunks = (a.Hq + a.heads - 1) / a.heads;
+    a.kchunks = (a.Hk + a.heads - 1) / a.heads;
+    a.units = a.tokens * (a.qchunks + a.kchunks);
+    if (a.units >= want || a.heads == 1) break;
+  }
   a.h_inner = a.tq.sh < a.tq.sn;
+  // backward: the resident CTAs, shared by q and k as their units are
+  const int64_t most = (int64_t)kBwdPerSm * sm_count();
+  const int64_t q = (a.tokens * a.qchunks + per - 1) / per;
+  const int64_t k = (a.tokens * a.kchunks + per - 1) / per;
+  if (q + k <= most) {
+    a.qblocks = (int)q;
+    a.kblocks = (int)k;
+  } else {
+    const int64_t kb = most * a.kchunks / (a.qchunks + a.kchunks);
+    a.kblocks = (int)imax64(1, imin64(kb, most - 1));
+    a.qblocks = (int)most - a.kblocks;
+  }
 }
 
 #define FLARE_LPG(kern, T, lpg, ...)                 \
@@ -397,9 +451,9 @@ flare_status_t flare_qk_norm_rope_fwd(const void* q, const void* k, const void* 
   a.eps = eps;
   a.cos = cos, a.sin = sin;
   a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.qo = qo, a.ko = ko;
-  cut(a, B);
-  note_error("%s", "");
   const int lpg = lanes_per_row(D, dt);
+  cut(a, B, lpg);
+  note_error("%s", "");
   const int64_t per = kThreads / lpg;
   const dim3 grid((unsigned)((a.units + per - 1) / per));
   cudaStream_t st = (cudaStream_t)stream;
@@ -418,8 +472,8 @@ size_t flare_qk_norm_rope_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int6
   if (check(B, Hq, Hk, N, D, 0, dt, none, none, 0, 1.f) != FLARE_OK) return 0;
   NormRopeArgs a = {};
   a.Hq = (int)Hq, a.Hk = (int)Hk, a.N = (int)N;
-  cut(a, B);
-  return (size_t)(bwd_blocks(a.units, lanes_per_row(D, dt)) * kPartBytes);
+  cut(a, B, lanes_per_row(D, dt));
+  return (size_t)(a.qblocks + a.kblocks) * 128 * sizeof(float);
 }
 
 flare_status_t flare_qk_norm_rope_bwd(const void* q, const void* k, const void* wq, const void* wk,
@@ -449,11 +503,10 @@ flare_status_t flare_qk_norm_rope_bwd(const void* q, const void* k, const void* 
   a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.dqo = dqo, a.dko = dko, a.dq = dq, a.dk = dk;
   a.dwq = dwq, a.dwk = dwk;
   a.part = (float*)workspace;
-  cut(a, B);
-  note_error("%s", "");
   const int lpg = lanes_per_row(D, dt);
-  const int64_t blocks = bwd_blocks(a.units, lpg);
-  const dim3 grid((unsigned)blocks);
+  cut(a, B, lpg);
+  note_error("%s", "");
+  const dim3 grid((unsigned)(a.qblocks + a.kblocks));
   cudaStream_t st = (cudaStream_t)stream;
   if (dt == FLARE_BF16) {
     FLARE_LPG(FLARE_BWD_KERNEL, __nv_bfloat16, lpg, a, grid, st);
@@ -463,11 +516,12 @@ flare_status_t flare_qk_norm_rope_bwd(const void* q, const void* k, const void* 
   if (dwq || dwk) {
     if (dt == FLARE_BF16)
       FLARE_CUDA(launch_pdl(norm_rope_dw_kernel<__nv_bfloat16>, dim3(8), dim3(256), 0, st,
-                            (const float*)a.part, (int)blocks, (int)D, (__nv_bfloat16*)dwq,
+                            (const float*)a.part, a.qblocks, a.kblocks, (int)D, (__nv_bfloat16*)dwq,
                             (__nv_bfloat16*)dwk));
     else
       FLARE_CUDA(launch_pdl(norm_rope_dw_kernel<float>, dim3(8), dim3(256), 0, st,
-                            (const float*)a.part, (int)blocks, (int)D, (float*)dwq, (float*)dwk));
+                            (const float*)a.part, a.qblocks, a.kblocks, (int)D, (float*)dwq,
+                            (float*)dwk));
   }
   FLARE_CUDA(cudaPeekAtLastError());
   return FLARE_OK;
