@@ -110,14 +110,14 @@ SIGNATURES = {
     "flare_exp_split": (_i32, [_i32, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_double)]),
     "flare_probe_mma_rate": (_i32, [_i32, _i32, _i32, _vp, _sz, ctypes.POINTER(ctypes.c_double),
                                     _vp]),
-    "flare_attn_fwd": (_i32, [_vp] * 4 + [_stp] + [_vp] * 2 + [_i64] * 6 +
+    "flare_attn_fwd": (_i32, [_vp] * 4 + [_vp] + [_vp] * 2 + [_i64] * 6 +
                        [_i32, _f32, _i32, _vp, _vp, _sz, _vp]),
-    "flare_attn_bwd": (_i32, [_vp] * 9 + [_stp] + [_vp] * 2 + [_i64] * 6 +
+    "flare_attn_bwd": (_i32, [_vp] * 9 + [_vp] + [_vp] * 2 + [_i64] * 6 +
                        [_i32, _f32, _i32, _vp, _sz, _vp]),
     "flare_attn_workspace_size": (_sz, [_i32] + [_i64] * 6 + [_i32]),
-    "flare_qk_norm_rope_fwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 2 + [_stp] + [_i64] * 6 +
+    "flare_qk_norm_rope_fwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 2 + [_vp] + [_i64] * 6 +
                                [_i32, _i32, _f32, _vp]),
-    "flare_qk_norm_rope_bwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 6 + [_stp] + [_i64] * 6 +
+    "flare_qk_norm_rope_bwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 6 + [_vp] + [_i64] * 6 +
                                [_i32, _i32, _f32, _vp, _sz, _vp]),
     "flare_qk_norm_rope_workspace_size": (_sz, [_i64] * 5 + [_i32]),
     "flare_selftest_wait_timeout": (_i32, [_vp, _sz, ctypes.c_uint64, _vp]),

@@ -8,7 +8,6 @@ and everything is computed in ``libflare.so``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import importlib
@@ -23,47 +22,78 @@ from ._lib import FlareError
 _f = importlib.import_module(__package__ + ".flare")
 
 
-def _on(device: torch.device, stream):
+# the current stream's handle by device index
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+class _NoSwitch:
+    """The tensors' device and the caller's stream are current already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(index: int, stream):
     """Makes the tensors' device, and ``stream`` when given, current: the
     call's buffers then belong to the stream that uses them."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if torch.cuda.current_device() != index:
+        return torch.cuda.device(index)
+    return _NO_SWITCH
 
 
-def _same(what: str, *ts):
-    """Checks 4-D views with D contiguous, of one device and dtype."""
-    first = ts[0]
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError(f"{what} tensors must live on a CUDA device")
-        if t.dim() != 4 or t.stride(-1) != 1:
+def _same(what: str, first, *ts) -> int:
+    """Checks 4-D views with D contiguous, of one device and dtype; returns
+    the device's index."""
+    index, dtype = first.get_device(), first.dtype
+    for t in (first, *ts):
+        if t.get_device() != index or index < 0:
+            raise ValueError(f"{what} tensors must live on one CUDA device")
+        if t.dim() != 4 or t.stride(3) != 1:
             raise ValueError(f"{what} tensors must be [B,H,N,D] views with D contiguous")
-        if t.device != first.device or t.dtype != first.dtype:
-            raise ValueError(f"{what} tensors differ in device or dtype")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} tensors differ in dtype")
+    return index
+
+
+_ARRAYS = {n: ctypes.c_int64 * (3 * n) for n in (4, 6, 8)}
+
+
+def _strides(*ts):
+    """The flare_strides_t array of these tensors."""
+    return _ARRAYS[len(ts)](*[s for t in ts for s in t.stride()[:3]])
 
 
 def _shape(name: str, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _rows(name: str, t, shape, device):
-    if t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(name: str, t, shape, index: int):
+    if t.dtype != torch.float32 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor on the tensors' device")
     _shape(name, t, shape)
 
 
-def _workspace(workspace, nbytes: int, device, where: str):
+def _workspace(workspace, nbytes: int, like, where: str):
     if workspace is None:
         if nbytes == 0:
             raise FlareError(2, where)
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.device != device \
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if workspace.dtype != torch.uint8 or workspace.get_device() != like.get_device() \
             or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
     return workspace
@@ -85,15 +115,16 @@ def attn_workspace_size(backward: bool, B: int, Hq: int, Hk: int, Nq: int, Nk: i
                                                      code))
 
 
-def _attn_dims(q, k, v):
-    _same("attention", q, k, v)
+def _attn_dims(q, k, v, *more):
+    """The device's index and the sizes."""
+    index = _same("attention", q, k, v, *more)
     B, Hq, Nq, D = q.shape
-    Hk, Nk = k.shape[1], k.shape[2]
+    _, Hk, Nk, _ = k.shape
     _shape("k", k, (B, Hk, Nk, D))
-    _shape("v", v, (B, Hk, Nk, D))
+    _shape("v", v, k.shape)
     if Hk == 0 or Hq % Hk:
         raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
-    return B, Hq, Hk, Nq, Nk, D
+    return index, B, Hq, Hk, Nq, Nk, D
 
 
 def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
@@ -110,26 +141,29 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
     valid queries and keys; rows past them are never used and y is 0 there.
     ``causal``: query i sees keys j <= i + (keys - queries), counted with the
     lengths.  A query that sees no key gives 0."""
-    B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
-    dev = q.device
+    index, B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
     code = _f._dtype_code(q)
-    s = _f.default_scale(D) if scale is None else float(scale)
-    ql, kl = _f._seq_lens(q_lens, B, dev), _f._seq_lens(k_lens, B, dev)
-    with _on(dev, stream):
-        y = torch.empty_like(q) if out is None else out
-        if out is not None:
-            _same("attention", q, out)
-            _shape("out", out, q.shape)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if save else None
-        ws = _workspace(workspace, _attn_bytes(0, B, Hq, Hk, Nq, Nk, D, code, dev.index), dev,
+    s = D ** -0.5 if scale is None else float(scale)
+    if q_lens is not None:
+        _f._seq_lens(q_lens, B, q.device)
+    if k_lens is not None:
+        _f._seq_lens(k_lens, B, q.device)
+    with _on(index, stream):
+        if out is None:
+            y = torch.empty_like(q)
+        else:
+            y = out
+            _same("attention", q, y)
+            _shape("out", y, q.shape)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if save else None
+        ws = _workspace(workspace, _attn_bytes(0, B, Hq, Hk, Nq, Nk, D, code, index), q,
                         "flare_attn_workspace_size")
         st = _lib.load().flare_attn_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _f._strides(q, k, v, y),
-            None if ql is None else ql.data_ptr(), None if kl is None else kl.data_ptr(),
-            B, Hq, Hk, Nq, Nk, D, code, s, int(bool(causal)),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-            torch.cuda.current_stream().cuda_stream)
-    _lib.check(st, "flare_attn_fwd")
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _strides(q, k, v, y),
+            _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s, 1 if causal else 0, _p(lse),
+            ws.data_ptr(), ws.numel(), _raw_stream(index))
+    if st:
+        _lib.check(st, "flare_attn_fwd")
     return (y, lse) if save else y
 
 
@@ -140,33 +174,32 @@ def attn_bwd(q, k, v, y, dy, lse, scale: Optional[float] = None, *, causal: bool
     """Gradients (dq, dk, dv) of attn_fwd for the upstream gradient dy, from
     its output y and lse (``save=True``).  ``need_dq`` / ``need_dkv``: what is
     not wanted is not computed and comes back as None."""
-    B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
-    _same("attention", q, y, dy)
+    index, B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v, y, dy)
     _shape("y", y, q.shape)
     _shape("dy", dy, q.shape)
-    dev = q.device
-    _rows("lse", lse, (B, Hq, Nq), dev)
+    _rows("lse", lse, (B, Hq, Nq), index)
     if not (need_dq or need_dkv):
         return None, None, None
     code = _f._dtype_code(q)
-    s = _f.default_scale(D) if scale is None else float(scale)
-    ql, kl = _f._seq_lens(q_lens, B, dev), _f._seq_lens(k_lens, B, dev)
-    with _on(dev, stream):
+    s = D ** -0.5 if scale is None else float(scale)
+    if q_lens is not None:
+        _f._seq_lens(q_lens, B, q.device)
+    if k_lens is not None:
+        _f._seq_lens(k_lens, B, q.device)
+    with _on(index, stream):
         dq = torch.empty_like(q) if need_dq else None
         dk = torch.empty_like(k) if need_dkv else None
         dv = torch.empty_like(v) if need_dkv else None
-        ws = _workspace(workspace, _attn_bytes(1, B, Hq, Hk, Nq, Nk, D, code, dev.index), dev,
+        ws = _workspace(workspace, _attn_bytes(1, B, Hq, Hk, Nq, Nk, D, code, index), q,
                         "flare_attn_workspace_size")
-        strides = _f._strides(q, k, v, y, dy, q if dq is None else dq, k if dk is None else dk,
-                              v if dv is None else dv)
+        strides = _strides(q, k, v, y, dy, dq if need_dq else q, dk if need_dkv else k,
+                           dv if need_dkv else v)
         st = _lib.load().flare_attn_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), dy.data_ptr(), lse.data_ptr(),
-            None if dq is None else dq.data_ptr(), None if dk is None else dk.data_ptr(),
-            None if dv is None else dv.data_ptr(), strides,
-            None if ql is None else ql.data_ptr(), None if kl is None else kl.data_ptr(),
-            B, Hq, Hk, Nq, Nk, D, code, s, int(bool(causal)), ws.data_ptr(), ws.numel(),
-            torch.cuda.current_stream().cuda_stream)
-    _lib.check(st, "flare_attn_bwd")
+            _p(dq), _p(dk), _p(dv), strides, _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s,
+            1 if causal else 0, ws.data_ptr(), ws.numel(), _raw_stream(index))
+    if st:
+        _lib.check(st, "flare_attn_bwd")
     return dq, dk, dv
 
 
@@ -177,33 +210,30 @@ def _norm_bytes(B, Hq, Hk, N, D, code: int, device: int) -> int:
     return int(_lib.load().flare_qk_norm_rope_workspace_size(B, Hq, Hk, N, D, code))
 
 
-def _norm_args(q, k, wq, wk, cos, sin):
-    """Sizes (B, Hq, Hk, N, D, R) and the table's batch stride."""
-    _same("query and key", q, k)
+def _norm_args(q, k, wq, wk, cos, sin, *more):
+    """The device's index, sizes (B, Hq, Hk, N, D, R), the table's batch stride."""
+    index = _same("query and key", q, k, *more)
     B, Hq, N, D = q.shape
-    _shape("k", k, (B, k.shape[1], N, D))
+    Hk = k.shape[1]
+    _shape("k", k, (B, Hk, N, D))
     for name, w in (("wq", wq), ("wk", wk)):
-        if w is None:
-            continue
-        if w.dtype != q.dtype or w.device != q.device or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of the heads' device and dtype")
-        _shape(name, w, (D,))
+        if w is not None:
+            if w.dtype != q.dtype or w.get_device() != index or not w.is_contiguous():
+                raise ValueError(
+                    f"{name} must be a contiguous tensor of the heads' device and dtype")
+            _shape(name, w, (D,))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    R, sb = 0, 0
-    if cos is not None:
-        R = 2 * cos.shape[-1]
-        shape = (B, N, R // 2) if cos.dim() == 3 else (N, R // 2)
-        _rows("cos", cos, shape, q.device)
-        _rows("sin", sin, shape, q.device)
-        sb = N * (R // 2) if cos.dim() == 3 else 0
-        if R == 0:
-            raise ValueError("cos and sin are empty; leave them out for no rotation")
-    return B, Hq, k.shape[1], N, D, R, sb
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
+    if cos is None:
+        return index, B, Hq, Hk, N, D, 0, 0
+    half = cos.shape[-1]
+    own = cos.dim() == 3
+    shape = (B, N, half) if own else (N, half)
+    _rows("cos", cos, shape, index)
+    _rows("sin", sin, shape, index)
+    if half == 0:
+        raise ValueError("cos and sin are empty; leave them out for no rotation")
+    return index, B, Hq, Hk, N, D, 2 * half, N * half if own else 0
 
 
 def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float = 1e-6,
@@ -218,9 +248,9 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float =
     up to 128.  Pairs are (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
     q and k may be any views with D contiguous; the outputs take their layout,
     or go to ``out`` = (qo, ko), which may be q and k themselves."""
-    B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
+    index, B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
     code = _f._dtype_code(q)
-    with _on(q.device, stream):
+    with _on(index, stream):
         if out is None:
             qo, ko = torch.empty_like(q), torch.empty_like(k)
         else:
@@ -230,9 +260,10 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float =
             _shape("out[1]", ko, k.shape)
         st = _lib.load().flare_qk_norm_rope_fwd(
             q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(cos), _p(sin), sb, qo.data_ptr(),
-            ko.data_ptr(), _f._strides(q, k, qo, ko), B, Hq, Hk, N, D, R, int(bool(interleaved)),
-            code, float(eps), torch.cuda.current_stream().cuda_stream)
-    _lib.check(st, "flare_qk_norm_rope_fwd")
+            ko.data_ptr(), _strides(q, k, qo, ko), B, Hq, Hk, N, D, R, 1 if interleaved else 0,
+            code, eps, _raw_stream(index))
+    if st:
+        _lib.check(st, "flare_qk_norm_rope_fwd")
     return qo, ko
 
 
@@ -241,24 +272,23 @@ def qk_norm_rope_bwd(q, k, wq, wk, cos, sin, dqo, dko, *, eps: float = 1e-6,
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients (dq, dk, dwq, dwk) of qk_norm_rope_fwd; dwq, dwk are None
     for weights that are None, or without ``need_dw``."""
-    B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
-    _same("query and key", q, dqo, dko)
+    index, B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin, dqo, dko)
     _shape("dqo", dqo, q.shape)
     _shape("dko", dko, k.shape)
     code = _f._dtype_code(q)
-    dev = q.device
-    with _on(dev, stream):
+    with _on(index, stream):
         dq, dk = torch.empty_like(q), torch.empty_like(k)
         dwq = torch.empty_like(wq) if need_dw and wq is not None else None
         dwk = torch.empty_like(wk) if need_dw and wk is not None else None
-        ws = _workspace(workspace, _norm_bytes(B, Hq, Hk, N, D, code, dev.index), dev,
+        ws = _workspace(workspace, _norm_bytes(B, Hq, Hk, N, D, code, index), q,
                         "flare_qk_norm_rope_workspace_size")
         st = _lib.load().flare_qk_norm_rope_bwd(
             q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(cos), _p(sin), sb, dqo.data_ptr(),
             dko.data_ptr(), dq.data_ptr(), dk.data_ptr(), _p(dwq), _p(dwk),
-            _f._strides(q, k, dqo, dko, dq, dk), B, Hq, Hk, N, D, R, int(bool(interleaved)), code,
-            float(eps), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
-    _lib.check(st, "flare_qk_norm_rope_bwd")
+            _strides(q, k, dqo, dko, dq, dk), B, Hq, Hk, N, D, R, 1 if interleaved else 0, code,
+            eps, ws.data_ptr(), ws.numel(), _raw_stream(index))
+    if st:
+        _lib.check(st, "flare_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -266,10 +296,23 @@ def qk_norm_rope_bwd(q, k, wq, wk, cos, sin, dqo, dko, *, eps: float = 1e-6,
 
 def _grad_view(t: torch.Tensor) -> torch.Tensor:
     """An upstream gradient the library reads in place, else a contiguous copy."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
     esz = t.element_size()
     ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
         n == 1 or (s > 0 and (s * esz) % 16 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
     return t if ok else t.contiguous()
+
+
+def _once(backward):
+    """A backward that cannot be differentiated again.  Where no graph is
+    built of it (the ordinary case) it runs without the wrapper's cost."""
+    guarded = once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return run
 
 
 class AttnFunction(torch.autograd.Function):
@@ -286,7 +329,7 @@ class AttnFunction(torch.autograd.Function):
         return y
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dy):
         q, k, v, y, lse, q_lens, k_lens = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -306,7 +349,7 @@ class QkNormRopeFunction(torch.autograd.Function):
         return qk_norm_rope_fwd(q, k, wq, wk, cos, sin, eps=eps, interleaved=interleaved)
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dqo, dko):
         q, k, wq, wk, cos, sin = ctx.saved_tensors
         need = ctx.needs_input_grad
