@@ -463,7 +463,7 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   char* ws = (char*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   AttnFwdArgs a = {};
-  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk), a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
   a.hpt = p.hpt, a.qblocks = (int)p.qblocks, a.splits = p.splits, a.causal = d.causal;
   a.units = p.units;
   a.c = scale * kLog2e;
@@ -517,7 +517,7 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   char* ws = (char*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   AttnBwdArgs a = {};
-  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk), a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
   a.tile = p.tile, a.ktiles = (int)p.ktiles, a.qtiles = (int)p.qtiles;
   a.dkv_splits = p.dkv_splits, a.dq_splits = p.dq_splits, a.causal = d.causal;
   a.dkv_units = p.dkv_units, a.dq_units = p.dq_units;

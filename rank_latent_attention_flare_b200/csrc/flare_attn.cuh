@@ -25,6 +25,7 @@ struct AttnDims {
 struct AttnSeq {
   int ql, kl, off;   // valid queries, valid keys; causal: key j <= query i + off
   bool causal;
+  __device__ __forceinline__ AttnSeq(int Nq, int Nk) : ql(Nq), kl(Nk), off(Nk - Nq), causal(false) {}
   __device__ __forceinline__ AttnSeq(const int32_t* q_lens, const int32_t* k_lens, int b, int Nq,
                                      int Nk, bool causal_)
       : ql(Nq), kl(Nk), causal(causal_) {
@@ -42,6 +43,19 @@ struct AttnSeq {
   // first tile of T queries of which some query sees key j
   __device__ __forceinline__ int first_query_tile(int j, int T) const {
     return causal ? max(0, j - off) / T : 0;
+  }
+};
+
+// Part `split` of `splits` near-equal parts of n tiles: [lo, lo + count).
+// (32-bit divisions here and in the kernels' indices: a 64-bit one costs as
+// much as a hundred instructions.)
+struct Part {
+  int lo, count;
+  __device__ __forceinline__ Part(int n, int split, int splits) : lo(0), count(n) {
+    if (splits == 1) return;
+    const int q = (int)((unsigned)n / (unsigned)splits), rem = n - q * splits;
+    lo = q * split + min(split, rem);
+    count = q + (split < rem);
   }
 };
 
@@ -109,7 +123,7 @@ __device__ __forceinline__ void attn_check_lens(const int32_t* q_lens, const int
 
 // Kernel arguments shared by the forward kernels.
 struct AttnFwdArgs {
-  int B, Hq, Hk, Nq, Nk, D;
+  int B, Hq, Hk, G, Nq, Nk, D;   // G = Hq / Hk
   int hpt, qblocks, splits, causal;
   int64_t units;
   float c;                 // scale * log2(e)
@@ -124,7 +138,7 @@ struct AttnFwdArgs {
 };
 
 struct AttnBwdArgs {
-  int B, Hq, Hk, Nq, Nk, D;
+  int B, Hq, Hk, G, Nq, Nk, D;   // G = Hq / Hk
   int tile, ktiles, qtiles, dkv_splits, dq_splits, causal;
   int64_t dkv_units, dq_units;
   float scale, c;

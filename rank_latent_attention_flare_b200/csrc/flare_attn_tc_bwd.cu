@@ -139,18 +139,110 @@ template <int DP>
 struct DkvLayout {
   using T = Tile<DP>;
   // ring of Q and dY tiles in the order Q0 dY0 Q1 dY1 ...
-  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 9 : 14;
-  static constexpr int NB = 2;   // buffers of (nl, delta)
-  static constexpr int K_OFF = 0;
-  static constexpr int V_OFF = T::BYTES;
-  static constexpr int RING_OFF = 2 * T::BYTES;
+  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 8 : 12;
+  static constexpr int KB = DP == 128 ? 1 : 2;   // buffers of K and V
+  static constexpr int NB = 2;                   // buffers of (nl, delta)
+  static constexpr int K_OFF = 0;                // [KB][K, V]
+  static constexpr int RING_OFF = 2 * KB * T::BYTES;
   static constexpr int NL_OFF = RING_OFF + SLOTS * T::BYTES;       // [NB][nl 128, delta 128]
   static constexpr int BAR_OFF = NL_OFF + NB * 1024;
-  static constexpr int NBARS = 2 * SLOTS + 1 + 2 * NB + 6 + 1;
+  static constexpr int NBARS = 2 * SLOTS + 4 + 2 * NB + 6 + 2;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int BYTES = MISC_OFF + 16;
 };
 
+// One piece of the work: key tile kt of key head hk of batch b, and one part
+// of the query tiles of the heads that share it (the tiles first ..
+// first + per - 1 of each head; this part: n of them from number lo).
+struct DkvItem {
+  int b, hk, kt, split, k0, krow0, first, per, lo, n;
+  unsigned bh;
+  AttnSeq sq;
+  __device__ __forceinline__ DkvItem(const AttnBwdArgs& A, unsigned idx) : sq(A.Nq, A.Nk) {
+    split = 0;
+    unsigned u = idx;
+    if (A.dkv_splits > 1) {
+      u = idx / (unsigned)A.dkv_splits;
+      split = (int)(idx - u * A.dkv_splits);
+    }
+    // causal: the keys that most queries see first
+    const unsigned inner = A.causal ? (unsigned)(A.B * A.Hk) : (unsigned)A.ktiles;
+    const unsigned hi = u / inner, rest = u - hi * inner;
+    kt = (int)(A.causal ? hi : rest);
+    bh = A.causal ? rest : hi;
+    b = (int)(bh / (unsigned)A.Hk);
+    hk = (int)bh - b * A.Hk;
+    sq = AttnSeq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
+    k0 = kt * kAttnTile;
+    krow0 = tile_row0(kt, kAttnTile, sq.kl);
+    first = sq.first_query_tile(k0, kAttnTile);
+    per = k0 < sq.kl ? max(0, (sq.ql + kAttnTile - 1) / kAttnTile - first) : 0;
+    const Part part(per * A.G, split, A.dkv_splits);
+    lo = part.lo;
+    n = part.count;
+  }
+};
+
+// The pieces of a CTA: one in each round of the grid, the order turned round
+// every other time, so that sorted pieces add up to about the same.
+struct Rounds {
+  unsigned total, base;   // total < 2^31
+  bool back;
+  __device__ __forceinline__ explicit Rounds(unsigned total_) : total(total_), base(0), back(false) {}
+  __device__ __forceinline__ bool more() const { return base < total; }
+  __device__ __forceinline__ unsigned index() const {
+    return base + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  }
+  __device__ __forceinline__ void next() {
+    base += gridDim.x;
+    back = !back;
+  }
+};
+
+// The query tiles of a piece in turn: head and tile number.
+struct QueryTiles {
+  int head, t, first, end;
+  __device__ __forceinline__ explicit QueryTiles(const DkvItem& w)
+      : head(w.lo > 0 ? w.lo / w.per : 0),
+        t(w.first + (w.lo > 0 ? w.lo - head * w.per : 0)),
+        first(w.first),
+        end(w.first + w.per) {}
+  __device__ __forceinline__ void next() {
+    if (++t == end) t = first, ++head;
+  }
+};
+
+// A place in a CTA's sequence of query tiles: tile j of n of piece c (those
+// without a query tile left out), the J-th of all.
+struct Cursor {
+  Rounds rd;
+  int n = 0, j = 0, c = -1, J = 0;
+  bool on = true;
+  __device__ __forceinline__ Cursor(const AttnBwdArgs& A, unsigned total) : rd(total) { piece(A); }
+  __device__ __forceinline__ void piece(const AttnBwdArgs& A) {
+    for (n = 0; rd.more(); rd.next()) {
+      if (rd.index() < rd.total) n = DkvItem(A, rd.index()).n;
+      if (n > 0) break;
+    }
+    on = n > 0;
+    j = 0;
+    ++c;
+  }
+  __device__ __forceinline__ bool last() const { return j + 1 == n; }
+  __device__ __forceinline__ void next(const AttnBwdArgs& A) {
+    ++J;
+    if (++j < n) return;
+    rd.next();
+    piece(A);
+  }
+};
+
+// A CTA may stay for several pieces.  Barriers count on through them: J is the
+// number of the query tile since the start, c that of the piece.  With two
+// buffers of K and V the products of a piece follow those of the one before
+// without a break, and its loads run ahead; the sums of a piece are stored
+// between the tiles.  Long pieces are better left to the hardware, one CTA
+// each: it hands them out as SMs become free.
 template <int KS>
 __global__ void __launch_bounds__(kBThreads, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -161,13 +253,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
   constexpr int DP = attn_dp(16 * KS);
   using L = DkvLayout<DP>;
   using T = Tile<DP>;
-  constexpr int NS = L::SLOTS, NB = L::NB;
+  constexpr int NS = L::SLOTS, NB = L::NB, KB = L::KB;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
   uint64_t* full = bars;               // [slot] tile landed
   uint64_t* empty = bars + NS;         // [slot] its last product is done
-  uint64_t* kv_full = bars + 2 * NS;
-  uint64_t* nl_full = kv_full + 1;     // [NB]
+  uint64_t* kv_full = bars + 2 * NS;   // [buffer of K and V]
+  uint64_t* kv_empty = kv_full + 2;    // [buffer] K and V of the piece are read
+  uint64_t* nl_full = kv_empty + 2;    // [NB]
   uint64_t* nl_empty = nl_full + NB;   // [NB]
   uint64_t* s_full = nl_empty + NB;    // [buffer of S]
   // [buffer of S]: with two of them a fast warp may be one tile ahead of a
@@ -175,7 +268,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
   uint64_t* p_ready = s_full + 2;
   uint64_t* dp_full = s_full + 4;
   uint64_t* ds_ready = s_full + 5;
-  uint64_t* done = s_full + 6;
+  uint64_t* done = s_full + 6;         // dK and dV of the piece are complete
+  uint64_t* acc_free = s_full + 7;     // and stored
   uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
   volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
   // S has two buffers where TMEM has room (SB = 2): S of tile j + 2 then
@@ -184,36 +278,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
   constexpr uint32_t TP = 128 * SB, TK = TP + 128, TV = TK + DP;   // S at 0
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- this CTA's work
-  int64_t u = blockIdx.x;
-  const int split = (int)(u % A.dkv_splits);
-  u /= A.dkv_splits;
-  int kt;
-  int64_t bh;
-  if (A.causal) {   // the keys that most queries see first
-    const int64_t BH = (int64_t)A.B * A.Hk;
-    kt = (int)(u / BH);
-    bh = u % BH;
-  } else {
-    kt = (int)(u % A.ktiles);
-    bh = u / A.ktiles;
-  }
-  const int b = (int)(bh / A.Hk), hk = (int)(bh % A.Hk), G = A.Hq / A.Hk;
-  const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
-  const int k0 = kt * kAttnTile;
-  const int krow0 = tile_row0(kt, kAttnTile, sq.kl);
-  const int first = sq.first_query_tile(k0, kAttnTile);
-  const int per = k0 < sq.kl ? max(0, (sq.ql + kAttnTile - 1) / kAttnTile - first) : 0;
-  const int lo = (int)((int64_t)per * G * split / A.dkv_splits);
-  int n = (int)((int64_t)per * G * (split + 1) / A.dkv_splits) - lo;
+  const int G = A.G;
+  unsigned total = (unsigned)(A.dkv_units * A.dkv_splits);
   if (smem_u32(smem) & 1023) {   // tiles and their descriptors need this alignment
-    n = 0;
+    total = 0;
     if (threadIdx.x == 0) record_error(A.err, kErrAttnDkvTmaWait);
   }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * NS + 1; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < 2 * NS + 4; ++s) mbar_init(&bars[s], 1);
     for (int s = 0; s < NB; ++s) {
       mbar_init(&nl_full[s], 1);
       mbar_init(&nl_empty[s], 16);
@@ -225,6 +298,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, 16);
     mbar_init(done, 1);
+    mbar_init(acc_free, 16);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -236,44 +310,57 @@ __global__ void __launch_bounds__(kBThreads, 1)
 
   if (warp == kBWarpTma) {
     // --------------------------------------------------------------- TMA
-    if (n > 0 && elect_one()) {
-      const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
-      const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
-      const int qb = (A.bcast & 1) ? 0 : b, gb = (A.bcast & 64) ? 0 : b;
-      mbar_arrive_expect_tx(kv_full, 2 * T::BYTES);
-      load_tile<DP>(smem + L::K_OFF, &tmK, kv_full, krow0, kh, kb);
-      load_tile<DP>(smem + L::V_OFF, &tmV, kv_full, krow0, vh, vb);
-      int last = -1;
-      for (int it = 0; it < 2 * n; ++it) {
-        const int s = it % NS, use = it / NS;
-        if (use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) {
-          record_error(A.err, kErrAttnDkvTmaWait);
-          *abort_flag = 1;
-          break;
+    if (elect_one()) {
+      bool ok = true;
+      int c = 0, it = 0;   // pieces and ring items so far
+      for (Rounds rd(total); ok && rd.more(); rd.next()) {
+        if (rd.index() >= total) continue;
+        const DkvItem w(A, rd.index());
+        if (w.n == 0) continue;
+        const int kb = (A.bcast & 2) ? 0 : w.b, kh = (A.bcast & 16) ? 0 : w.hk;
+        const int vb = (A.bcast & 4) ? 0 : w.b, vh = (A.bcast & 32) ? 0 : w.hk;
+        const int qb = (A.bcast & 1) ? 0 : w.b, gb = (A.bcast & 64) ? 0 : w.b;
+        const int kvb = c % KB, used = c / KB;
+        if (used > 0 && !(ok = mbar_wait(&kv_empty[kvb], (uint32_t)((used - 1) & 1)))) break;
+        uint8_t* kv = smem + L::K_OFF + kvb * 2 * T::BYTES;
+        mbar_arrive_expect_tx(&kv_full[kvb], 2 * T::BYTES);
+        load_tile<DP>(kv, &tmK, &kv_full[kvb], w.krow0, kh, kb);
+        load_tile<DP>(kv + T::BYTES, &tmV, &kv_full[kvb], w.krow0, vh, vb);
+        ++c;
+        QueryTiles qt(w);
+        for (int j = 0; ok && j < w.n; ++j, qt.next()) {
+          const int h = w.hk * G + qt.head;
+          const int row = tile_row0(qt.t, kAttnTile, w.sq.ql);
+          for (int k = 0; k < 2; ++k, ++it) {
+            const int s = it % NS, use = it / NS;
+            if ((use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) || *abort_flag) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
+            mbar_arrive_expect_tx(&full[s], T::BYTES);
+            if (k) load_tile<DP>(dst, &tmG, &full[s], row, (A.bcast & 128) ? 0 : h, gb);
+            else load_tile<DP>(dst, &tmQ, &full[s], row, (A.bcast & 8) ? 0 : h, qb);
+          }
         }
-        if (*abort_flag) break;
-        const int x = lo + (it >> 1);
-        const int h = hk * G + x / per;
-        const int row = tile_row0(first + x % per, kAttnTile, sq.ql);
-        uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
-        mbar_arrive_expect_tx(&full[s], T::BYTES);
-        if (it & 1) load_tile<DP>(dst, &tmG, &full[s], row, (A.bcast & 128) ? 0 : h, gb);
-        else load_tile<DP>(dst, &tmQ, &full[s], row, (A.bcast & 8) ? 0 : h, qb);
-        last = it;
+      }
+      if (!ok) {
+        record_error(A.err, kErrAttnDkvTmaWait);
+        *abort_flag = 1;
       }
       // every load lands before the CTA can exit
-      for (int it = max(0, last - NS + 1); it <= last; ++it)
-        mbar_wait_sleep(&full[it % NS], (uint32_t)((it / NS) & 1));
-      mbar_wait_sleep(kv_full, 0);
+      for (int x = max(0, it - NS); x < it; ++x)
+        mbar_wait_sleep(&full[x % NS], (uint32_t)((x / NS) & 1));
+      for (int x = max(0, c - KB); x < c; ++x)
+        mbar_wait_sleep(&kv_full[x % KB], (uint32_t)((x / KB) & 1));
     }
     __syncwarp();
   } else if (warp == kBWarpMma) {
     // --------------------------------------------------------------- MMA
-    if (n > 0 && elect_one()) {
+    if (elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
       const uint64_t dK = T::k_major(smem_u32(smem + L::K_OFF));
-      const uint64_t dV = T::k_major(smem_u32(smem + L::V_OFF));
       const uint32_t ring = smem_u32(smem + L::RING_OFF);
       const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
       auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
@@ -295,44 +382,71 @@ __global__ void __launch_bounds__(kBThreads, 1)
                  (!start || kk > 0) ? 1u : 0u);
         mma_commit(&empty[it % NS]);
       };
-      auto issue_S = [&](int j) {
-        issue_nt(128 * (j % SB), dK, 2 * j, &s_full[j % SB]);
+      auto kv = [&](int c) { return dK + ((uint32_t)((c % KB) * 2 * T::BYTES) >> 4); };
+      // S or dP of the tile at a cursor; K and V of its piece have landed
+      auto issue_S = [&](const Cursor& x) -> bool {
+        if (x.j == 0 && !mbar_wait(&kv_full[x.c % KB], (uint32_t)((x.c / KB) & 1))) return false;
+        if (!landed(2 * x.J)) return false;
+        tc_fence_after();
+        issue_nt(128 * (x.J % SB), kv(x.c), 2 * x.J, &s_full[x.J % SB]);
+        return true;
       };
-      bool ok = mbar_wait(kv_full, 0) && landed(0) && landed(1);
-      if (ok) {
+      auto issue_dP = [&](const Cursor& x) -> bool {
+        if (!landed(2 * x.J + 1)) return false;
         tc_fence_after();
-        issue_S(0);
-        issue_nt(TP, dV, 1, dp_full);
-      }
-      if (SB == 2 && ok && n > 1 && (ok = landed(2))) {
-        tc_fence_after();
-        issue_S(1);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = mbar_wait(&p_ready[j % SB], (uint32_t)((j / SB) & 1)))) break;
-        tc_fence_after();
-        issue_nn(TV, 128 * (j % SB), 2 * j + 1, j == 0);
-        if (j + SB < n) {
-          if (!(ok = landed(2 * (j + SB)))) break;
-          tc_fence_after();
-          issue_S(j + SB);
+        issue_nt(TP, kv(x.c) + (T::BYTES >> 4), 2 * x.J + 1, dp_full);
+        if (x.last()) mma_commit(&kv_empty[x.c % KB]);   // S was issued before
+        return true;
+      };
+      // x: the tile whose dV and dK come next; xs, xp: the next S and dP
+      Cursor x(A, total), xs = x, xp = x;
+      bool ok = true;
+      // S runs SB tiles ahead, dP one; into the next piece only where its K
+      // and V have a buffer of their own
+      auto may = [&](const Cursor& y) { return y.on && (KB == 2 || y.c == x.c); };
+      int c = 0;   // pieces complete
+      while (x.on) {
+        if (x.j == 0 && (KB == 1 || x.J == 0)) {   // nothing of this piece is under way
+          for (int k = 0; ok && k < SB && may(xs); ++k) {
+            if ((ok = issue_S(xs))) xs.next(A);
+            if (k == 0 && ok && (ok = issue_dP(xp))) xp.next(A);
+          }
+          if (!ok) break;
         }
-        if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
+        const int J = x.J;
+        if (!(ok = mbar_wait(&p_ready[J % SB], (uint32_t)((J / SB) & 1)))) break;
+        if (x.j == 0 && c > 0 && !(ok = mbar_wait(acc_free, (uint32_t)((c - 1) & 1)))) break;
         tc_fence_after();
-        issue_nn(TK, TP, 2 * j, j == 0);
-        if (j + 1 < n) {
-          if (!(ok = landed(2 * j + 3))) break;
-          tc_fence_after();
-          issue_nt(TP, dV, 2 * j + 3, dp_full);
+        issue_nn(TV, 128 * (J % SB), 2 * J + 1, x.j == 0);
+        if (may(xs)) {
+          if (!(ok = issue_S(xs))) break;
+          xs.next(A);
         }
-        if (*abort_flag) ok = false;
+        if (!(ok = mbar_wait(ds_ready, (uint32_t)(J & 1)))) break;
+        tc_fence_after();
+        issue_nn(TK, TP, 2 * J, x.j == 0);
+        if (x.last()) {
+          mma_commit(done);
+          ++c;
+        }
+        if (may(xp)) {
+          if (!(ok = issue_dP(xp))) break;
+          xp.next(A);
+        }
+        if (*abort_flag) {
+          ok = false;
+          break;
+        }
+        x.next(A);
       }
       if (!ok) {
         record_error(A.err, kErrAttnDkvMmaWait);
         *abort_flag = 1;
+        mma_commit(done);
+        ++c;
       }
-      mma_commit(done);
-      mbar_wait_sleep(done, 0);
+      // every product is complete before the CTA can exit
+      if (c > 0) mbar_wait_sleep(done, (uint32_t)((c - 1) & 1));
     }
     __syncwarp();
   } else if (warp == kBWarpAux) {
@@ -340,22 +454,27 @@ __global__ void __launch_bounds__(kBThreads, 1)
     // Columns before the tile's own queries (a last tile moved back) get
     // nl = -inf: weight 0.
     bool ok = true;
-    for (int j = 0; ok && j < n; ++j) {
-      const int s = j % NB, use = j / NB;
-      if (use > 0) ok = warp_all(mbar_wait_sleep(&nl_empty[s], (uint32_t)((use - 1) & 1)));
-      if (!ok) break;
-      const int x = lo + j, t = first + x % per;
-      const int row0 = tile_row0(t, kAttnTile, sq.ql);
-      const int64_t base = ((int64_t)b * A.Hq + hk * G + x / per) * A.Nq;
-      float* dst = (float*)(smem + L::NL_OFF + s * 1024);
+    int J = 0;
+    for (Rounds rd(total); ok && rd.more(); rd.next()) {
+      if (rd.index() >= total) continue;
+      const DkvItem w(A, rd.index());
+      QueryTiles qt(w);
+      for (int j = 0; j < w.n; ++j, ++J, qt.next()) {
+        const int s = J % NB, use = J / NB;
+        if (use > 0) ok = warp_all(mbar_wait_sleep(&nl_empty[s], (uint32_t)((use - 1) & 1)));
+        if (!ok) break;
+        const int row0 = tile_row0(qt.t, kAttnTile, w.sq.ql);
+        const int64_t base = ((int64_t)w.b * A.Hq + w.hk * G + qt.head) * A.Nq;
+        float* dst = (float*)(smem + L::NL_OFF + s * 1024);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int col = 32 * k + lane, q = row0 + col;
-        const bool own = q >= t * kAttnTile;
-        dst[col] = own ? A.nl[base + q] : -INFINITY;
-        dst[128 + col] = own ? A.delta[base + q] : 0.f;
+        for (int k = 0; k < 4; ++k) {
+          const int col = 32 * k + lane, q = row0 + col;
+          const bool own = q >= qt.t * kAttnTile;
+          dst[col] = own ? A.nl[base + q] : -INFINITY;
+          dst[128 + col] = own ? A.delta[base + q] : 0.f;
+        }
+        warp_arrive(&nl_full[s]);
       }
-      warp_arrive(&nl_full[s]);
     }
     if (!ok) {
       record_error(A.err, kErrAttnDkvRowWait);
@@ -368,84 +487,96 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tP = tmem + lb + TP + kCols * w;
     bool ok = true;
-    int t = first + (n > 0 ? lo % per : 0);   // the query tile
-    for (int j = 0; j < n; ++j) {
-      const int s = j % NB;
-      const uint32_t tS = tmem + lb + 128 * (j % SB) + kCols * w;
-      const int row0 = tile_row0(t, kAttnTile, sq.ql);
-      if (++t == first + per) t = first;
-      // columns below cl do not see this lane's key
-      const int cl = sq.causal ? krow0 + r - sq.off - row0 - kCols * w : -1;
-      const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
-      if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((j / NB) & 1)))) {
-        ok = false;
-        break;
-      }
-      float nv[kCols];   // read ahead of the wait for S
+    int c = 0, J = 0;
+    for (Rounds rd(total); ok && rd.more(); rd.next()) {
+      if (rd.index() >= total) continue;
+      const DkvItem it(A, rd.index());
+      QueryTiles qt(it);
+      for (int j = 0; j < it.n; ++j, ++J, qt.next()) {
+        const int s = J % NB;
+        const uint32_t tS = tmem + lb + 128 * (J % SB) + kCols * w;
+        const int row0 = tile_row0(qt.t, kAttnTile, it.sq.ql);
+        // columns below cl do not see this lane's key
+        const int cl = it.sq.causal ? it.krow0 + r - it.sq.off - row0 - kCols * w : -1;
+        const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
+        if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((J / NB) & 1)))) {
+          ok = false;
+          break;
+        }
+        float nv[kCols];   // read ahead of the wait for S
 #pragma unroll
-      for (int x = 0; x < kCols; x += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(nl + x);
-        nv[x] = v.x, nv[x + 1] = v.y, nv[x + 2] = v.z, nv[x + 3] = v.w;
+        for (int x = 0; x < kCols; x += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(nl + x);
+          nv[x] = v.x, nv[x + 1] = v.y, nv[x + 2] = v.z, nv[x + 3] = v.w;
+        }
+        const bool gone = nl[lane] == -INFINITY;
+        if (!warp_all(mbar_wait(&s_full[J % SB], (uint32_t)((J / SB) & 1)))) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        uint32_t p[kCols];
+        tmem_ld32(tS, p);
+        tmem_wait_ld_dep(p);
+        // a tile with masked columns or rows without weight keeps to the MUFU,
+        // whose exponential of -inf is 0
+        if (warp_any(cl > 0 || gone)) {
+          mask_cols(p, 0, cl, kCols - 1);
+          exp_cols<true, 0>(p, A.c, 0.f, nv);
+        } else {
+          exp_cols<true, kBwdPoly>(p, A.c, 0.f, nv);
+        }
+        store_bf16_tmem(tS, p);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&p_ready[J % SB]);
+        if (!warp_all(mbar_wait(dp_full, (uint32_t)(J & 1)))) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        uint32_t g[kCols];
+        tmem_ld32(tP, g);
+        tmem_wait_ld_dep(g);
+        ds_cols<true>(g, p, 0.f, nl + 128);
+        warp_arrive(&nl_empty[s]);
+        store_bf16_tmem(tP, g);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(ds_ready);
       }
-      const bool gone = nl[lane] == -INFINITY;
-      if (!warp_all(mbar_wait(&s_full[j % SB], (uint32_t)((j / SB) & 1)))) {
-        ok = false;
-        break;
-      }
+      if (ok && it.n > 0) ok = warp_all(mbar_wait(done, (uint32_t)(c & 1)));
+      if (!ok) break;
       __syncwarp();
       tc_fence_after();
-      uint32_t p[kCols];
-      tmem_ld32(tS, p);
-      tmem_wait_ld_dep(p);
-      // a tile with masked columns or rows without weight keeps to the MUFU,
-      // whose exponential of -inf is 0
-      if (warp_any(cl > 0 || gone)) {
-        mask_cols(p, 0, cl, kCols - 1);
-        exp_cols<true, 0>(p, A.c, 0.f, nv);
-      } else {
-        exp_cols<true, kBwdPoly>(p, A.c, 0.f, nv);
+      // warpgroups 0 and 1 store dK, 2 and 3 dV: this tile's own keys, then
+      // zeros for the rows past the length
+      const int key = it.krow0 + r, v = w >> 1;
+      const Tok& to = v ? A.dv : A.dk;
+      __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + it.b * to.sb + it.hk * to.sh;
+      float* rec = nullptr;
+      if (A.dkv_splits > 1)
+        rec = A.dkv_part +
+              ((((int64_t)it.bh * A.ktiles + it.kt) * A.dkv_splits + it.split) * 2 + v) * kAttnTile * DP;
+      const bool own = key >= it.k0 && key < it.sq.kl;
+      put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, it.n > 0, it.n > 0, v ? 1.f : A.scale,
+                  out + key * to.sn, rec ? rec + (int64_t)(key - it.k0) * DP : nullptr, own, A.D);
+      if (it.n > 0) {
+        tc_fence_before();
+        warp_arrive(acc_free);
+        ++c;
       }
-      store_bf16_tmem(tS, p);
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(&p_ready[j % SB]);
-      if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
-        ok = false;
-        break;
-      }
+      if ((w & 1) && !rec && it.k0 + r >= it.sq.kl && it.k0 + r < A.Nk)
+        for (int d = 0; d < A.D; d += 8)
+          *reinterpret_cast<uint4*>(out + (it.k0 + r) * to.sn + d) = make_uint4(0, 0, 0, 0);
       __syncwarp();
-      tc_fence_after();
-      uint32_t g[kCols];
-      tmem_ld32(tP, g);
-      tmem_wait_ld_dep(g);
-      ds_cols<true>(g, p, 0.f, nl + 128);
-      warp_arrive(&nl_empty[s]);
-      store_bf16_tmem(tP, g);
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(ds_ready);
     }
-    if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
     if (!ok) {
       record_error(A.err, kErrAttnDkvRowWait);
       *abort_flag = 1;
     }
-    __syncwarp();
-    tc_fence_after();
-    // warpgroups 0 and 1 store dK, 2 and 3 dV: this tile's own keys, then
-    // zeros for the rows past the length
-    const int key = krow0 + r, v = w >> 1;
-    const Tok& to = v ? A.dv : A.dk;
-    __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + b * to.sb + hk * to.sh;
-    float* rec = nullptr;
-    if (A.dkv_splits > 1)
-      rec = A.dkv_part + (((bh * A.ktiles + kt) * A.dkv_splits + split) * 2 + v) * (int64_t)kAttnTile * DP;
-    const bool own = key >= k0 && key < sq.kl;
-    put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, n > 0, n > 0, v ? 1.f : A.scale,
-                out + key * to.sn, rec ? rec + (int64_t)(key - k0) * DP : nullptr, own, A.D);
-    if ((w & 1) && !rec && k0 + r >= sq.kl && k0 + r < A.Nk)
-      for (int d = 0; d < A.D; d += 8)
-        *reinterpret_cast<uint4*>(out + (k0 + r) * to.sn + d) = make_uint4(0, 0, 0, 0);
   }
   __syncwarp();
   tc_fence_before();
@@ -497,25 +628,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- this CTA's work
-  int64_t u = blockIdx.x;
-  const int split = (int)(u % A.dq_splits);
-  u /= A.dq_splits;
-  int qt;
-  int64_t bh;
-  if (A.causal) {   // longest rows first
-    const int64_t BH = (int64_t)A.B * A.Hq;
-    qt = A.qtiles - 1 - (int)(u / BH);
-    bh = u % BH;
-  } else {
-    qt = (int)(u % A.qtiles);
-    bh = u / A.qtiles;
+  unsigned u = blockIdx.x;
+  int split = 0;
+  if (A.dq_splits > 1) {
+    u = blockIdx.x / (unsigned)A.dq_splits;
+    split = (int)(blockIdx.x - u * A.dq_splits);
   }
-  const int b = (int)(bh / A.Hq), h = (int)(bh % A.Hq), hk = h / (A.Hq / A.Hk);
+  // causal: longest rows first
+  const unsigned inner = A.causal ? (unsigned)(A.B * A.Hq) : (unsigned)A.qtiles;
+  const unsigned hi = u / inner, rest = u - hi * inner;
+  const int qt = A.causal ? A.qtiles - 1 - (int)hi : (int)rest;
+  const int64_t bh = A.causal ? rest : hi;
+  const int b = (int)bh / A.Hq, h = (int)bh - b * A.Hq, hk = h / A.G;
   const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
   const int q0 = qt * kAttnTile;
-  const int nall = q0 < sq.ql ? sq.key_tiles(q0 + kAttnTile - 1, kAttnTile) : 0;
-  const int lo = (int)((int64_t)nall * split / A.dq_splits);
-  int n = (int)((int64_t)nall * (split + 1) / A.dq_splits) - lo;
+  const Part part(q0 < sq.ql ? sq.key_tiles(q0 + kAttnTile - 1, kAttnTile) : 0, split, A.dq_splits);
+  const int lo = part.lo;
+  int n = part.count;
   if (smem_u32(smem) & 1023) {   // tiles and their descriptors need this alignment
     n = 0;
     if (threadIdx.x == 0) record_error(A.err, kErrAttnDqTmaWait);
@@ -720,8 +849,12 @@ cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
     r = launch_pdl(kernel, dim3((unsigned)grid), kBThreads, smem, st, mq, mk, mv, mg, a);
     return r != cudaSuccess ? r : cudaPeekAtLastError();
   };
-  if (a.dK && (e = go(attn_dkv_kernel<KS>, p.dkv_units * p.dkv_splits, DkvLayout<DP>::BYTES)) !=
-                  cudaSuccess)
+  // CTAs stay for several pieces where a piece is short (256 latents over
+  // 65,536 tokens, D 64: 2 query tiles a piece)
+  const int64_t pieces = p.dkv_units * p.dkv_splits;
+  const bool stay = DkvLayout<DP>::KB == 2 && d.G() * p.qtiles <= 8 * p.dkv_splits;
+  if (a.dK && (e = go(attn_dkv_kernel<KS>, stay ? imin64(pieces, sm_count()) : pieces,
+                      DkvLayout<DP>::BYTES)) != cudaSuccess)
     return e;
   if (a.dQ) e = go(attn_dq_kernel<KS>, p.dq_units * p.dq_splits, DqLayout<DP>::BYTES);
   return e;

@@ -104,22 +104,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's work
   const int hgroups = A.Hq / A.hpt;              // head groups per batch element
-  int64_t u = blockIdx.x;
-  const int split = (int)(u % A.splits);
-  u /= A.splits;
-  int qb;
-  int64_t bhg;
-  if (A.causal) {   // longest rows first
-    const int64_t BHG = (int64_t)A.B * hgroups;
-    qb = A.qblocks - 1 - (int)(u / BHG);
-    bhg = u % BHG;
-  } else {          // the query blocks of a head together: they share its keys in L2
-    qb = (int)(u % A.qblocks);
-    bhg = u / A.qblocks;
+  unsigned u = blockIdx.x;
+  int split = 0;
+  if (A.splits > 1) {
+    u = blockIdx.x / (unsigned)A.splits;
+    split = (int)(blockIdx.x - u * A.splits);
   }
-  const int b = (int)(bhg / hgroups);
-  const int h0 = (int)(bhg % hgroups) * A.hpt;
-  const int hk = h0 / (A.Hq / A.Hk);
+  // causal: longest rows first; else the query blocks of a head together:
+  // they share its keys in L2
+  const unsigned inner = A.causal ? (unsigned)(A.B * hgroups) : (unsigned)A.qblocks;
+  const unsigned uh = u / inner, ur = u - uh * inner;
+  const int qb = A.causal ? A.qblocks - 1 - (int)uh : (int)ur;
+  const int64_t bhg = A.causal ? ur : uh;
+  const int b = (int)bhg / hgroups;
+  const int h0 = ((int)bhg - b * hgroups) * A.hpt;
+  const int hk = h0 / A.G;
   const int64_t rec = ((bhg * A.qblocks + qb) * A.splits + split) * (QT * 128);
   const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
   const bool packed = A.hpt > 1;
@@ -133,9 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (QT == 1) nt[1] = nt[0];
   const int nall = max(nt[0], nt[1]);
-  const int lo = (int)((int64_t)nall * split / A.splits);
-  const int hi = (int)((int64_t)nall * (split + 1) / A.splits);
-  const int n = hi - lo;
+  const Part part(nall, split, A.splits);
+  const int lo = part.lo, n = part.count, hi = lo + n;
   const int n0 = max(0, min(hi, nt[0]) - lo), n1 = max(0, min(hi, nt[1]) - lo);
 
   if (threadIdx.x == 0) {
