@@ -123,6 +123,27 @@ __device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* p, float v) {
   *p = __float2bfloat16_rn(v);
 }
 
+// row = (b H + h) N + i.  32-bit divisions where they reach.
+struct RowOf {
+  int i, h;
+  int64_t b, bh;
+  __device__ __forceinline__ RowOf(int64_t row, int N, int H) {
+    if (row <= 0x7fffffffLL) {
+      const unsigned r = (unsigned)row, x = r / (unsigned)N;
+      i = (int)(r - x * N);
+      const unsigned y = x / (unsigned)H;
+      h = (int)(x - y * H);
+      b = y;
+      bh = x;
+    } else {
+      bh = row / N;
+      i = (int)(row - bh * N);
+      b = bh / H;
+      h = (int)(bh - b * H);
+    }
+  }
+};
+
 // Joins the records (ref, sum, O) of the splits of one query row: weights
 // 2^(ref_s - max ref), added in split order (the result does not depend on
 // timing).  One warp per row, DP / 32 columns per lane.  Bound by latency:
@@ -136,10 +157,9 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (row >= (int64_t)A.B * A.Hq * A.Nq) return;
-  const int i = (int)(row % A.Nq);
-  const int64_t bh = row / A.Nq;
-  const int h = (int)(bh % A.Hq);
-  const int64_t b = bh / A.Hq;
+  const RowOf at(row, A.Nq, A.Hq);
+  const int i = at.i, h = at.h;
+  const int64_t b = at.b, bh = at.bh;
   // where the forward kernel put the row
   int64_t unit;
   int r;
@@ -197,10 +217,9 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __grid_constan
   const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LP;
   const int sub = threadIdx.x % LP;
   const bool in = row < (int64_t)A.B * A.Hq * A.Nq;
-  const int i = (int)(row % A.Nq);
-  const int64_t bh = row / A.Nq;
-  const int h = (int)(bh % A.Hq);
-  const int64_t b = bh / A.Hq;
+  const RowOf at(in ? row : 0, A.Nq, A.Hq);
+  const int i = at.i, h = at.h;
+  const int64_t b = at.b;
   bool live = in;
   if (in && A.q_lens) live = i < A.q_lens[b];
   float s = 0.f;
@@ -243,10 +262,9 @@ __global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const __grid_constant
   const int col = (int)(id % C) * 4;
   const int64_t row = id / C;
   if (row >= (int64_t)A.B * H * N || col >= A.D) return;
-  const int n = (int)(row % N);
-  const int64_t bh = row / N;
-  const int h = (int)(bh % H);
-  const int64_t b = bh / H;
+  const RowOf at(row, N, H);
+  const int n = at.i, h = at.h;
+  const int64_t b = at.b, bh = at.bh;
   const int32_t* lens = WHICH ? A.k_lens : A.q_lens;
   const bool own = lens == nullptr || n < lens[b];
   const int64_t unit = bh * tiles + n / A.tile;

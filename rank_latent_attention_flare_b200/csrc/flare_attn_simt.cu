@@ -1,21 +1,22 @@
 // Softmax attention forward and backward on the CUDA cores: float32 inputs,
 // whose products the tensor cores' bf16 operands would round.
 //
-// Tiles of 64 queries x 64 keys, 256 threads, each with 4 x 4 logits: thread
-// (ty, tx) = (tid / 16, tid % 16) owns rows 4 ty + i and columns tx + 16 c.
+// Tiles of 64 queries x 64 keys, 128 threads, each with 8 x 4 logits: thread
+// (ty, tx) = (tid / 16, tid % 16) owns rows 8 ty + i and columns tx + 16 c.
 // Every product is one of two loops over shared memory:
 //   nt: C[r][c] += sum_d A[r][d] B[c][d]      (logits, dP)
 //   nn: C[r][e] += sum_k P[r][k] B[k][e]      (O, dV, dK, dQ)
 // Rows are padded by 4 floats, so that both are free of bank conflicts.
-// Bound: 16 FMAs per 8 (nt) or per 4 + E/4 (nn, E columns a thread) 16-byte
-// shared-memory reads, i.e. by the FMA pipe and shared memory about equally.
+// Bound: 128 FMAs per 12 (nt) or per 8 + E (nn, E columns a thread) 16-byte
+// shared-memory reads, i.e. by shared memory and the FMA pipe about equally.
 #include "flare_attn.cuh"
 
 namespace flare {
 namespace {
 
 constexpr int kT = 64;             // queries and keys per tile
-constexpr int kNT = 256;
+constexpr int kNT = 128;
+constexpr int kR = 8;              // rows per thread
 constexpr int kPS = kT + 4;        // row pitch of a 64 x 64 tile
 
 // Rows [row0, row0 + 64) of p, the first n valid rows and D columns of it;
@@ -35,20 +36,20 @@ __device__ __forceinline__ void load_rows(float* dst, const float* p, int64_t sn
 
 template <int DP>
 __device__ __forceinline__ void prod_nt(const float* A, const float* B, int ty, int tx,
-                                        float (&c)[4][4]) {
+                                        float (&c)[kR][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 a[4], b[4];
+    float4 a[kR], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *(const float4*)(A + (4 * ty + i) * (DP + 4) + d);
+    for (int i = 0; i < kR; ++i) a[i] = *(const float4*)(A + (kR * ty + i) * (DP + 4) + d);
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = *(const float4*)(B + (tx + 16 * j) * (DP + 4) + d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         c[i][j] = fmaf(a[i].x, b[j].x, c[i][j]);
@@ -69,14 +70,14 @@ struct Cols {
 
 template <int DP>
 __device__ __forceinline__ void prod_nn(const float* P, const float* B, int ty, int tx,
-                                        float (&c)[4][DP / 16]) {
+                                        float (&c)[kR][DP / 16]) {
   using C = Cols<DP>;
 #pragma unroll 2
   for (int k = 0; k < kT; k += 4) {
-    float p[4][4];
+    float p[kR][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = *(const float4*)(P + (4 * ty + i) * kPS + k);
+    for (int i = 0; i < kR; ++i) {
+      const float4 v = *(const float4*)(P + (kR * ty + i) * kPS + k);
       p[i][0] = v.x, p[i][1] = v.y, p[i][2] = v.z, p[i][3] = v.w;
     }
 #pragma unroll
@@ -93,7 +94,7 @@ __device__ __forceinline__ void prod_nn(const float* P, const float* B, int ty, 
           b[0] = v.x, b[1] = v.y;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kR; ++i)
 #pragma unroll
           for (int w = 0; w < C::W; ++w)
             c[i][g * C::W + w] = fmaf(p[i][q], b[w], c[i][g * C::W + w]);
@@ -101,34 +102,34 @@ __device__ __forceinline__ void prod_nn(const float* P, const float* B, int ty, 
   }
 }
 
-// Writes a thread's 4 rows times f as rows [row0, n) of a token tensor.
+// Writes a thread's rows times f as rows [row0, n) of a token tensor.
 template <int DP>
 __device__ __forceinline__ void put_rows(float* p, int64_t sn, int row0, int n, int D, int ty, int tx,
-                                         const float (&c)[4][DP / 16], const float (&f)[4]) {
+                                         const float (&c)[kR][DP / 16], float f) {
   using C = Cols<DP>;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + 4 * ty + i;
+  for (int i = 0; i < kR; ++i) {
+    const int r = row0 + kR * ty + i;
     if (r >= n) continue;
 #pragma unroll
     for (int g = 0; g < C::NG; ++g)
 #pragma unroll
       for (int w = 0; w < C::W; ++w) {
         const int col = C::at(tx, g) + w;
-        if (col < D) p[r * sn + col] = c[i][g * C::W + w] * f[i];
+        if (col < D) p[r * sn + col] = c[i][g * C::W + w] * f;
       }
   }
 }
 
-// Writes a thread's 4 rows to a float32 record [64][DP].
+// Writes a thread's rows to a float32 record [64][DP].
 template <int DP>
-__device__ __forceinline__ void put_part(float* p, int ty, int tx, const float (&c)[4][DP / 16]) {
+__device__ __forceinline__ void put_part(float* p, int ty, int tx, const float (&c)[kR][DP / 16]) {
   using C = Cols<DP>;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kR; ++i)
 #pragma unroll
     for (int e = 0; e < C::E; ++e)
-      p[(4 * ty + i) * DP + C::at(tx, e / C::W) + e % C::W] = c[i][e];
+      p[(kR * ty + i) * DP + C::at(tx, e / C::W) + e % C::W] = c[i][e];
 }
 
 __device__ __forceinline__ float row_max(float v) {
@@ -166,22 +167,24 @@ __global__ void __launch_bounds__(kNT)
   const int hgroups = A.Hq / A.hpt;
   const int split = (int)(blockIdx.x % A.splits);
   const int u = blockIdx.x / A.splits;
-  const int qb = A.qblocks - 1 - u % A.qblocks;   // the longest rows of a causal mask first
-  const int bhg = u / A.qblocks;
+  // causal: the longest rows of all heads first
+  const int BHG = A.B * hgroups;
+  const int qb = A.causal ? A.qblocks - 1 - u / BHG : u % A.qblocks;
+  const int bhg = A.causal ? u % BHG : u / A.qblocks;
   const int b = bhg / hgroups, h0 = (bhg % hgroups) * A.hpt, hk = h0 / (A.Hq / A.Hk);
   const int64_t rec = (((int64_t)bhg * A.qblocks + qb) * A.splits + split) * kT;
   const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
   const bool packed = A.hpt > 1;
   const int q0 = qb * kT;
   const int nall = q0 < sq.ql ? sq.key_tiles(packed ? A.Nq - 1 : q0 + kT - 1, kT) : 0;
-  const int lo = (int)((int64_t)nall * split / A.splits);
-  const int hi = (int)((int64_t)nall * (split + 1) / A.splits);
+  const Part part(nall, split, A.splits);
+  const int lo = part.lo, hi = lo + part.count;
 
-  int qi[4], qh[4];
-  bool live[4];
+  int qi[kR], qh[kR];
+  bool live[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < kR; ++i) {
+    const int r = kR * ty + i;
     qh[i] = packed ? h0 + min(r / A.Nq, A.hpt - 1) : h0;
     qi[i] = packed ? r % A.Nq : q0 + r;
     live[i] = packed ? r < A.hpt * A.Nq : qi[i] < A.Nq;
@@ -202,9 +205,9 @@ __global__ void __launch_bounds__(kNT)
     load_rows<DP>(qs, Q + b * A.q.sb + h0 * A.q.sh, A.q.sn, q0, sq.ql, A.D);
   }
 
-  float m[4], l[4], o[4][DP / 16];
+  float m[kR], l[kR], o[kR][DP / 16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kR; ++i) {
     m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
     for (int e = 0; e < DP / 16; ++e) o[i][e] = 0.f;
@@ -216,10 +219,10 @@ __global__ void __launch_bounds__(kNT)
     load_rows<DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
     load_rows<DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
     __syncthreads();
-    float s[4][4];
+    float s[kR][4];
     prod_nt<DP>(qs, ks, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       const int last = sq.causal ? min(sq.kl - 1, qi[i] + sq.off) : sq.kl - 1;
       float mx = -INFINITY;
 #pragma unroll
@@ -243,24 +246,24 @@ __global__ void __launch_bounds__(kNT)
     }
     __syncthreads();   // the key tile is read
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ks[(4 * ty + i) * kPS + tx + 16 * j] = s[i][j];
+      for (int j = 0; j < 4; ++j) ks[(kR * ty + i) * kPS + tx + 16 * j] = s[i][j];
     __syncthreads();
     prod_nn<DP>(ks, vs, ty, tx, o);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) l[i] = row_sum(l[i]);   // each thread held 4 columns of its rows
+  for (int i = 0; i < kR; ++i) l[i] = row_sum(l[i]);   // each thread held 4 columns of its rows
   if (A.splits > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
       if (tx == 0 && live[i])
-        A.part_ml[rec + 4 * ty + i] = make_float2(m[i], qi[i] < sq.ql ? l[i] : 0.f);
+        A.part_ml[rec + kR * ty + i] = make_float2(m[i], qi[i] < sq.ql ? l[i] : 0.f);
     put_part<DP>(A.part_o + rec * DP, ty, tx, o);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kR; ++i) {
     if (!live[i]) continue;
     const bool some = qi[i] < sq.ql && l[i] != 0.f;
     float* y = (float*)A.Y + b * A.y.sb + qh[i] * A.y.sh + qi[i] * A.y.sn;
@@ -293,18 +296,19 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const int split = (int)(blockIdx.x % A.dkv_splits);
   const int unit = blockIdx.x / A.dkv_splits;
-  const int kt = unit % A.ktiles;
-  const int bh = unit / A.ktiles;
+  const int BH = A.B * A.Hk;
+  const int kt = A.causal ? unit / BH : unit % A.ktiles;
+  const int bh = A.causal ? unit % BH : unit / A.ktiles;
   const int b = bh / A.Hk, hk = bh % A.Hk, G = A.Hq / A.Hk;
   const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
   const int k0 = kt * kT;
   const int first = sq.first_query_tile(k0, kT);
   const int per = k0 < sq.kl ? max(0, (sq.ql + kT - 1) / kT - first) : 0;   // tiles of a head
-  const int lo = (int)((int64_t)per * G * split / A.dkv_splits);
-  const int hi = (int)((int64_t)per * G * (split + 1) / A.dkv_splits);
+  const Part part(per * G, split, A.dkv_splits);
+  const int lo = part.lo, hi = lo + part.count;
   load_rows<DP>(ks, (const float*)A.K + b * A.k.sb + hk * A.k.sh, A.k.sn, k0, sq.kl, A.D);
   load_rows<DP>(vs, (const float*)A.V + b * A.v.sb + hk * A.v.sh, A.v.sn, k0, sq.kl, A.D);
-  float dk[4][DP / 16] = {}, dv[4][DP / 16] = {};
+  float dk[kR][DP / 16] = {}, dv[kR][DP / 16] = {};
   for (int it = lo; it < hi; ++it) {
     const int h = hk * G + it / per, q0 = (first + it % per) * kT;
     __syncthreads();
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
       dls[threadIdx.x] = in ? A.delta[row] : 0.f;
     }
     __syncthreads();
-    float s[4][4], dp[4][4];
+    float s[kR][4], dp[kR][4];
     prod_nt<DP>(ks, qs, ty, tx, s);
     prod_nt<DP>(vs, gs, ty, tx, dp);
 #pragma unroll
@@ -326,11 +330,11 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
       const float nl = nls[q], dl = dls[q];
       const int last = sq.causal ? min(sq.kl - 1, q0 + q + sq.off) : sq.kl - 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool seen = k0 + 4 * ty + i <= last && nl != -INFINITY;
+      for (int i = 0; i < kR; ++i) {
+        const bool seen = k0 + kR * ty + i <= last && nl != -INFINITY;
         s[i][j] = seen ? exp2f(fmaf(s[i][j], A.c, nl)) : 0.f;
         dp[i][j] = seen ? s[i][j] * (dp[i][j] - dl) : 0.f;
-        ps[(4 * ty + i) * kPS + q] = s[i][j];
+        ps[(kR * ty + i) * kPS + q] = s[i][j];
       }
     }
     __syncthreads();
@@ -339,19 +343,18 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ps[(4 * ty + i) * kPS + tx + 16 * j] = dp[i][j];
+      for (int i = 0; i < kR; ++i) ps[(kR * ty + i) * kPS + tx + 16 * j] = dp[i][j];
     __syncthreads();
     prod_nn<DP>(ps, qs, ty, tx, dk);
   }
   if (A.dkv_splits > 1) {
-    float* p = A.dkv_part + ((int64_t)unit * A.dkv_splits + split) * 2 * kT * DP;
+    float* p = A.dkv_part + (((int64_t)bh * A.ktiles + kt) * A.dkv_splits + split) * 2 * kT * DP;
     put_part<DP>(p, ty, tx, dk);
     put_part<DP>(p + kT * DP, ty, tx, dv);
     return;
   }
-  const float fs[4] = {A.scale, A.scale, A.scale, A.scale}, f1[4] = {1.f, 1.f, 1.f, 1.f};
-  put_rows<DP>((float*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk, fs);
-  put_rows<DP>((float*)A.dV + b * A.dv.sb + hk * A.dv.sh, A.dv.sn, k0, A.Nk, A.D, ty, tx, dv, f1);
+  put_rows<DP>((float*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk, A.scale);
+  put_rows<DP>((float*)A.dV + b * A.dv.sb + hk * A.dv.sh, A.dv.sn, k0, A.Nk, A.D, ty, tx, dv, 1.f);
 }
 
 // dQ of 64 queries: over the key tiles they see, dQ += (P (dY V^T - delta)) K.
@@ -368,25 +371,26 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const int split = (int)(blockIdx.x % A.dq_splits);
   const int unit = blockIdx.x / A.dq_splits;
-  const int qt = A.qtiles - 1 - unit % A.qtiles;
-  const int bh = unit / A.qtiles;
+  const int BH = A.B * A.Hq;
+  const int qt = A.causal ? A.qtiles - 1 - unit / BH : unit % A.qtiles;
+  const int bh = A.causal ? unit % BH : unit / A.qtiles;
   const int b = bh / A.Hq, h = bh % A.Hq, hk = h / (A.Hq / A.Hk);
   const AttnSeq sq(A.q_lens, A.k_lens, b, A.Nq, A.Nk, A.causal != 0);
   const int q0 = qt * kT;
   const int nall = q0 < sq.ql ? sq.key_tiles(q0 + kT - 1, kT) : 0;
-  const int lo = (int)((int64_t)nall * split / A.dq_splits);
-  const int hi = (int)((int64_t)nall * (split + 1) / A.dq_splits);
+  const Part part(nall, split, A.dq_splits);
+  const int lo = part.lo, hi = lo + part.count;
   load_rows<DP>(qs, (const float*)A.Q + b * A.q.sb + h * A.q.sh, A.q.sn, q0, sq.ql, A.D);
   load_rows<DP>(gs, (const float*)A.dY + b * A.dy.sb + h * A.dy.sh, A.dy.sn, q0, sq.ql, A.D);
-  float nl[4], dl[4];
+  float nl[kR], dl[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int q = q0 + 4 * ty + i;
+  for (int i = 0; i < kR; ++i) {
+    const int q = q0 + kR * ty + i;
     const int64_t row = ((int64_t)b * A.Hq + h) * A.Nq + q;
     nl[i] = q < sq.ql ? A.nl[row] : -INFINITY;
     dl[i] = q < sq.ql ? A.delta[row] : 0.f;
   }
-  float dq[4][DP / 16] = {};
+  float dq[kR][DP / 16] = {};
   const float* kp = (const float*)A.K + b * A.k.sb + hk * A.k.sh;
   const float* vp = (const float*)A.V + b * A.v.sb + hk * A.v.sh;
   for (int t = lo; t < hi; ++t) {
@@ -394,18 +398,18 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
     load_rows<DP>(ks, kp, A.k.sn, t * kT, sq.kl, A.D);
     load_rows<DP>(vs, vp, A.v.sn, t * kT, sq.kl, A.D);
     __syncthreads();
-    float s[4][4], dp[4][4];
+    float s[kR][4], dp[kR][4];
     prod_nt<DP>(qs, ks, ty, tx, s);
     prod_nt<DP>(gs, vs, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       const int last =
-          sq.causal ? min(sq.kl - 1, q0 + 4 * ty + i + sq.off) : sq.kl - 1;
+          sq.causal ? min(sq.kl - 1, q0 + kR * ty + i + sq.off) : sq.kl - 1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool seen = t * kT + tx + 16 * j <= last && nl[i] != -INFINITY;
         const float p = seen ? exp2f(fmaf(s[i][j], A.c, nl[i])) : 0.f;
-        ps[(4 * ty + i) * kPS + tx + 16 * j] = seen ? p * (dp[i][j] - dl[i]) : 0.f;
+        ps[(kR * ty + i) * kPS + tx + 16 * j] = seen ? p * (dp[i][j] - dl[i]) : 0.f;
       }
     }
     __syncthreads();
@@ -417,8 +421,7 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
                  tx, dq);
     return;
   }
-  const float fs[4] = {A.scale, A.scale, A.scale, A.scale};
-  put_rows<DP>((float*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq, fs);
+  put_rows<DP>((float*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq, A.scale);
 }
 
 template <typename... KA, typename... As>
