@@ -148,7 +148,8 @@ struct DkvLayout {
   static constexpr int BAR_OFF = NL_OFF + NB * 1024;
   static constexpr int NBARS = 2 * SLOTS + 4 + 2 * NB + 6 + 2;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int BYTES = MISC_OFF + 16;
+  static constexpr int ITEM_OFF = MISC_OFF + 32;   // [4] pieces, for the softmax warps
+  static constexpr int BYTES = ITEM_OFF + 4 * 64;
 };
 
 // One piece of the work: key tile kt of key head hk of batch b, and one part
@@ -158,6 +159,7 @@ struct DkvItem {
   int b, hk, kt, split, k0, krow0, first, per, lo, n;
   unsigned bh;
   AttnSeq sq;
+  __device__ __forceinline__ explicit DkvItem(const AttnBwdArgs& A) : n(0), sq(A.Nq, A.Nk) {}
   __device__ __forceinline__ DkvItem(const AttnBwdArgs& A, unsigned idx) : sq(A.Nq, A.Nk) {
     split = 0;
     unsigned u = idx;
@@ -182,6 +184,8 @@ struct DkvItem {
     n = part.count;
   }
 };
+
+static_assert(sizeof(DkvItem) <= 64, "a slot of the ring of pieces");
 
 // The pieces of a CTA: one in each round of the grid, the order turned round
 // every other time, so that sorted pieces add up to about the same.
@@ -212,28 +216,29 @@ struct QueryTiles {
   }
 };
 
-// A place in a CTA's sequence of query tiles: tile j of n of piece c (those
-// without a query tile left out), the J-th of all.
+// A place in the MMA thread's sequence of query tiles: tile j of n of piece c
+// (those without a query tile left out), the J-th of all.  The first cursor to
+// reach a piece finds its length, the others read it from ns[c % 4].
 struct Cursor {
-  Rounds rd;
   int n = 0, j = 0, c = -1, J = 0;
-  bool on = true;
-  __device__ __forceinline__ Cursor(const AttnBwdArgs& A, unsigned total) : rd(total) { piece(A); }
-  __device__ __forceinline__ void piece(const AttnBwdArgs& A) {
-    for (n = 0; rd.more(); rd.next()) {
+  __device__ __forceinline__ void find(const AttnBwdArgs& A, Rounds& rd, volatile int* ns) {
+    for (n = 0; rd.more() && n == 0; rd.next())
       if (rd.index() < rd.total) n = DkvItem(A, rd.index()).n;
-      if (n > 0) break;
-    }
-    on = n > 0;
     j = 0;
     ++c;
+    ns[c & 3] = n;
   }
+  __device__ __forceinline__ void follow(const volatile int* ns) {
+    j = 0;
+    ++c;
+    n = ns[c & 3];
+  }
+  __device__ __forceinline__ bool on() const { return n > 0; }
   __device__ __forceinline__ bool last() const { return j + 1 == n; }
-  __device__ __forceinline__ void next(const AttnBwdArgs& A) {
+  // to the next tile; true at the end of the piece
+  __device__ __forceinline__ bool step() {
     ++J;
-    if (++j < n) return;
-    rd.next();
-    piece(A);
+    return ++j == n;
   }
 };
 
@@ -272,6 +277,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   uint64_t* acc_free = s_full + 7;     // and stored
   uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
   volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
+  volatile int* ns = (volatile int*)(smem + L::MISC_OFF + 16);   // [4]
   // S has two buffers where TMEM has room (SB = 2): S of tile j + 2 then
   // follows dV of tile j, and the softmax never waits for it
   constexpr int SB = DP <= 64 ? 2 : 1;
@@ -399,17 +405,27 @@ __global__ void __launch_bounds__(kBThreads, 1)
         return true;
       };
       // x: the tile whose dV and dK come next; xs, xp: the next S and dP
-      Cursor x(A, total), xs = x, xp = x;
+      Cursor x, xs, xp;
+      Rounds rd(total);
       bool ok = true;
+      auto next_S = [&]() {
+        if (xs.step()) xs.find(A, rd, ns);
+      };
+      auto next_dP = [&]() {
+        if (xp.step()) xp.follow(ns);
+      };
+      xs.find(A, rd, ns);
+      xp.follow(ns);
+      x.follow(ns);
       // S runs SB tiles ahead, dP one; into the next piece only where its K
       // and V have a buffer of their own
-      auto may = [&](const Cursor& y) { return y.on && (KB == 2 || y.c == x.c); };
+      auto may = [&](const Cursor& y) { return y.on() && (KB == 2 || y.c == x.c); };
       int c = 0;   // pieces complete
-      while (x.on) {
+      while (x.on()) {
         if (x.j == 0 && (KB == 1 || x.J == 0)) {   // nothing of this piece is under way
           for (int k = 0; ok && k < SB && may(xs); ++k) {
-            if ((ok = issue_S(xs))) xs.next(A);
-            if (k == 0 && ok && (ok = issue_dP(xp))) xp.next(A);
+            if ((ok = issue_S(xs))) next_S();
+            if (k == 0 && ok && (ok = issue_dP(xp))) next_dP();
           }
           if (!ok) break;
         }
@@ -420,7 +436,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         issue_nn(TV, 128 * (J % SB), 2 * J + 1, x.j == 0);
         if (may(xs)) {
           if (!(ok = issue_S(xs))) break;
-          xs.next(A);
+          next_S();
         }
         if (!(ok = mbar_wait(ds_ready, (uint32_t)(J & 1)))) break;
         tc_fence_after();
@@ -431,13 +447,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
         }
         if (may(xp)) {
           if (!(ok = issue_dP(xp))) break;
-          xp.next(A);
+          next_dP();
         }
         if (*abort_flag) {
           ok = false;
           break;
         }
-        x.next(A);
+        if (x.step()) x.follow(ns);
       }
       if (!ok) {
         record_error(A.err, kErrAttnDkvMmaWait);
@@ -452,17 +468,46 @@ __global__ void __launch_bounds__(kBThreads, 1)
   } else if (warp == kBWarpAux) {
     // --------------------------- nl and delta of each tile's 128 columns
     // Columns before the tile's own queries (a last tile moved back) get
-    // nl = -inf: weight 0.
+    // nl = -inf: weight 0.  With a piece's first tile goes the piece itself,
+    // one without a tile at the end; pieces without a tile are zeros, written
+    // here.
     bool ok = true;
-    int J = 0;
+    int J = 0, c = 0;
+    auto slot_free = [&]() -> bool {
+      const int use = J / NB;
+      return use == 0 || warp_all(mbar_wait_sleep(&nl_empty[J % NB], (uint32_t)((use - 1) & 1)));
+    };
     for (Rounds rd(total); ok && rd.more(); rd.next()) {
       if (rd.index() >= total) continue;
       const DkvItem w(A, rd.index());
+      if (w.n == 0) {
+        const int rows = min(kAttnTile, A.Nk - w.k0);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int v = 0; v < 2; ++v) {
+          const Tok& to = v ? A.dv : A.dk;
+          __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + w.b * to.sb + w.hk * to.sh;
+          float* rec = A.dkv_part + ((((int64_t)w.bh * A.ktiles + w.kt) * A.dkv_splits + w.split) * 2 + v) *
+                                        kAttnTile * DP;
+          if (A.dkv_splits > 1) {
+            for (int x = lane; x < kAttnTile * DP / 4; x += 32) reinterpret_cast<uint4*>(rec)[x] = zero;
+          } else {
+            const int per_row = A.D / 8;
+            for (int x = lane; x < rows * per_row; x += 32) {
+              const int row = x / per_row;
+              *reinterpret_cast<uint4*>(out + (w.k0 + row) * to.sn + (x - row * per_row) * 8) = zero;
+            }
+          }
+        }
+        continue;
+      }
       QueryTiles qt(w);
       for (int j = 0; j < w.n; ++j, ++J, qt.next()) {
-        const int s = J % NB, use = J / NB;
-        if (use > 0) ok = warp_all(mbar_wait_sleep(&nl_empty[s], (uint32_t)((use - 1) & 1)));
-        if (!ok) break;
+        const int s = J % NB;
+        if (!(ok = slot_free())) break;
+        if (j == 0) {
+          if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = w;
+          ++c;
+        }
         const int row0 = tile_row0(qt.t, kAttnTile, w.sq.ql);
         const int64_t base = ((int64_t)w.b * A.Hq + w.hk * G + qt.head) * A.Nq;
         float* dst = (float*)(smem + L::NL_OFF + s * 1024);
@@ -476,6 +521,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
         warp_arrive(&nl_full[s]);
       }
     }
+    if (ok && (ok = slot_free())) {
+      if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = DkvItem(A);
+      warp_arrive(&nl_full[J % NB]);
+    }
     if (!ok) {
       record_error(A.err, kErrAttnDkvRowWait);
       *abort_flag = 1;
@@ -487,10 +536,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tP = tmem + lb + TP + kCols * w;
     bool ok = true;
-    int c = 0, J = 0;
-    for (Rounds rd(total); ok && rd.more(); rd.next()) {
-      if (rd.index() >= total) continue;
-      const DkvItem it(A, rd.index());
+    int J = 0;
+    for (int c = 0;; ++c) {
+      if (!(ok = warp_all(mbar_wait(&nl_full[J % NB], (uint32_t)((J / NB) & 1))))) break;
+      const DkvItem it = *(const DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64);
+      if (it.n == 0) break;
       QueryTiles qt(it);
       for (int j = 0; j < it.n; ++j, ++J, qt.next()) {
         const int s = J % NB;
@@ -547,8 +597,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tc_fence_before();
         warp_arrive(ds_ready);
       }
-      if (ok && it.n > 0) ok = warp_all(mbar_wait(done, (uint32_t)(c & 1)));
-      if (!ok) break;
+      if (!ok || !(ok = warp_all(mbar_wait(done, (uint32_t)(c & 1))))) break;
       __syncwarp();
       tc_fence_after();
       // warpgroups 0 and 1 store dK, 2 and 3 dV: this tile's own keys, then
@@ -561,13 +610,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
         rec = A.dkv_part +
               ((((int64_t)it.bh * A.ktiles + it.kt) * A.dkv_splits + it.split) * 2 + v) * kAttnTile * DP;
       const bool own = key >= it.k0 && key < it.sq.kl;
-      put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, it.n > 0, it.n > 0, v ? 1.f : A.scale,
+      put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, true, true, v ? 1.f : A.scale,
                   out + key * to.sn, rec ? rec + (int64_t)(key - it.k0) * DP : nullptr, own, A.D);
-      if (it.n > 0) {
-        tc_fence_before();
-        warp_arrive(acc_free);
-        ++c;
-      }
+      tc_fence_before();
+      warp_arrive(acc_free);
       if ((w & 1) && !rec && it.k0 + r >= it.sq.kl && it.k0 + r < A.Nk)
         for (int d = 0; d < A.D; d += 8)
           *reinterpret_cast<uint4*>(out + (it.k0 + r) * to.sn + d) = make_uint4(0, 0, 0, 0);
