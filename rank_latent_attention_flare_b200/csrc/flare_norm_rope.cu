@@ -201,6 +201,15 @@ __global__ void __launch_bounds__(kThreads, 3)
   const T* x = (const T*)(isk ? A.k : A.q) + b * ti.sb + n * ti.sn + h0 * ti.sh + d;
   T* y = (T*)(isk ? A.ko : A.qo) + b * to.sb + n * to.sn + h0 * to.sh + d;
   const void* w = isk ? A.wk : A.wq;
+  uint4 raw[U];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (h + j < cnt) raw[j] = *reinterpret_cast<const uint4*>(x + (h + j) * ti.sh);
+    }
+  };
+  load(0);   // in flight while the coefficients are built
   // y = r (x ca + x' cb)
   uint64_t ca[P], cb[P];
   int src;
@@ -219,12 +228,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   const float inv = 1.f / A.D;
   for (int h = 0; h < A.heads; h += U) {
-    uint4 raw[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      raw[j] = make_uint4(0, 0, 0, 0);
-      if (h + j < cnt) raw[j] = *reinterpret_cast<const uint4*>(x + (h + j) * ti.sh);
-    }
+    if (h > 0) load(h);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       uint64_t f[P], o[P], ss = 0;
@@ -271,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm)
     unit_of(A, on ? id : 0, chunks, b, n, ch);
     const int h0 = ch * A.heads;
     const int cnt = on && d < A.D ? min(A.heads, H - h0) : 0;
-    Angles<T> ang;
-    ang.load(A, b, n, d);
-    const int src = lane + (ang.other - d) / V;
     const T* x = (const T*)(isk ? A.k : A.q) + b * ti.sb + n * ti.sn + h0 * ti.sh + d;
     const T* g = (const T*)(isk ? A.dko : A.dqo) + b * tg.sb + n * tg.sn + h0 * tg.sh + d;
     T* dx = (T*)(isk ? A.dk : A.dq) + b * to.sb + n * to.sn + h0 * to.sh + d;
+    Angles<T> ang;
+    ang.load(A, b, n, d);
+    const int src = lane + (ang.other - d) / V;
     for (int h = 0; h < A.heads; h += U) {
       uint4 rx[U], rg[U];
 #pragma unroll
