@@ -562,6 +562,8 @@ FLARE_API flare_status_t flare_eval_exp2(const float* x, float* y, int64_t n, in
  *             with the lengths, so that the last query sees the last key.  A
  *             query that sees no key has Y = 0 and lse = -inf.
  *   lse_save  NULL, or float32 [B,Hq,Nq]: log of the softmax's denominator.
+ *   y_low_save  NULL, or a tensor laid out as Y (FLARE_BF16; ignored with
+ *             FLARE_F32): what rounding Y to bf16 left over, for the backward.
  *   workspace flare_attn_workspace_size(0, ...) bytes, 256-byte aligned.
  *
  * Supported: D a multiple of 8 up to 128; Nq, Nk <= 2^30; B Hq <= 65535;
@@ -573,7 +575,8 @@ FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void
                                         const flare_strides_t* strides, const int32_t* q_lens,
                                         const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk,
                                         int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dtype,
-                                        float scale, int causal, float* lse_save, void* workspace,
+                                        float scale, int causal, float* lse_save,
+                                        void* y_low_save, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
 /*
@@ -583,11 +586,13 @@ FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void
  *   dK = scale dS^T Q,
  * dK and dV summed over the query heads of a key head.  dQ, or dK and dV
  * together, may be NULL (not wanted).  Gradients of rows past the lengths are
- * 0; dY and Y are not read there.  strides: NULL or 8 entries: Q, K, V, Y,
- * dY, dQ, dK, dV.  workspace: flare_attn_workspace_size(1, ...) bytes.
+ * 0; dY and Y are not read there.  y_low: NULL, or flare_attn_fwd's
+ * y_low_save; with it sum_d dY Y is free of Y's rounding, which is otherwise
+ * the larger part of the error of dQ and dK beyond their own roundings.
+ * strides: NULL or 8 entries: Q, K, V, Y (and y_low), dY, dQ, dK, dV.  workspace: flare_attn_workspace_size(1, ...) bytes.
  */
 FLARE_API flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
-                                        const void* dY, const float* lse, void* dQ, void* dK,
+                                        const void* y_low, const void* dY, const float* lse, void* dQ, void* dK,
                                         void* dV, const flare_strides_t* strides,
                                         const int32_t* q_lens, const int32_t* k_lens, int64_t B,
                                         int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D,

@@ -111,8 +111,8 @@ SIGNATURES = {
     "flare_probe_mma_rate": (_i32, [_i32, _i32, _i32, _vp, _sz, ctypes.POINTER(ctypes.c_double),
                                     _vp]),
     "flare_attn_fwd": (_i32, [_vp] * 4 + [_vp] + [_vp] * 2 + [_i64] * 6 +
-                       [_i32, _f32, _i32, _vp, _vp, _sz, _vp]),
-    "flare_attn_bwd": (_i32, [_vp] * 9 + [_vp] + [_vp] * 2 + [_i64] * 6 +
+                       [_i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "flare_attn_bwd": (_i32, [_vp] * 10 + [_vp] + [_vp] * 2 + [_i64] * 6 +
                        [_i32, _f32, _i32, _vp, _sz, _vp]),
     "flare_attn_workspace_size": (_sz, [_i32] + [_i64] * 6 + [_i32]),
     "flare_qk_norm_rope_fwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 2 + [_vp] + [_i64] * 6 +

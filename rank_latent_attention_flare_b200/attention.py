@@ -129,10 +129,12 @@ def _attn_dims(q, k, v, *more):
 
 def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
              q_lens: Optional[torch.Tensor] = None, k_lens: Optional[torch.Tensor] = None,
-             save: bool = False, workspace: Optional[torch.Tensor] = None,
+             save: bool = False, save_low: bool = False,
+             workspace: Optional[torch.Tensor] = None,
              out: Optional[torch.Tensor] = None, stream=None):
     """Softmax attention softmax(scale q k^T) v.  Returns y, or (y, lse) when
-    ``save`` (lse float32 [B,Hq,Nq], for attn_bwd).
+    ``save`` (lse float32 [B,Hq,Nq], for attn_bwd), or (y, lse, y_low) when
+    ``save_low``: y_low is what rounding y to bf16 left over (None in float32).
 
     q [B,Hq,Nq,D]; k, v [B,Hk,Nk,D] with Hq a multiple of Hk (the query heads
     of a key head are neighbours); D a multiple of 8 up to 128.  All may be
@@ -155,29 +157,43 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
             y = out
             _same("attention", q, y)
             _shape("out", y, q.shape)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if save else None
+        lse = low = None
+        if save or save_low:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        if save_low and code == _lib.FLARE_BF16:
+            # y's own strides, also where ``out`` is a slice of something larger
+            low = torch.empty_like(y)
+            if low.stride() != y.stride():
+                raise ValueError("save_low takes an out without gaps")
         ws = _workspace(workspace, _attn_bytes(0, B, Hq, Hk, Nq, Nk, D, code, index), q,
                         "flare_attn_workspace_size")
         st = _lib.load().flare_attn_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _strides(q, k, v, y),
             _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s, 1 if causal else 0, _p(lse),
-            ws.data_ptr(), ws.numel(), _raw_stream(index))
+            _p(low), ws.data_ptr(), ws.numel(), _raw_stream(index))
     if st:
         _lib.check(st, "flare_attn_fwd")
+    if save_low:
+        return y, lse, low
     return (y, lse) if save else y
 
 
 def attn_bwd(q, k, v, y, dy, lse, scale: Optional[float] = None, *, causal: bool = False,
              q_lens: Optional[torch.Tensor] = None, k_lens: Optional[torch.Tensor] = None,
-             need_dq: bool = True, need_dkv: bool = True,
+             need_dq: bool = True, need_dkv: bool = True, y_low: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients (dq, dk, dv) of attn_fwd for the upstream gradient dy, from
-    its output y and lse (``save=True``).  ``need_dq`` / ``need_dkv``: what is
+    its output y and lse (``save=True``); with ``y_low`` (``save_low=True``) the
+    rounding of y does not enter the gradients.  ``need_dq`` / ``need_dkv``: what is
     not wanted is not computed and comes back as None."""
     index, B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v, y, dy)
     _shape("y", y, q.shape)
     _shape("dy", dy, q.shape)
     _rows("lse", lse, (B, Hq, Nq), index)
+    if y_low is not None:
+        _same("attention", y, y_low)
+        if y_low.shape != y.shape or y_low.stride() != y.stride():
+            raise ValueError("y_low must be laid out as y")
     if not (need_dq or need_dkv):
         return None, None, None
     code = _f._dtype_code(q)
@@ -195,8 +211,8 @@ def attn_bwd(q, k, v, y, dy, lse, scale: Optional[float] = None, *, causal: bool
         strides = _strides(q, k, v, y, dy, dq if need_dq else q, dk if need_dkv else k,
                            dv if need_dkv else v)
         st = _lib.load().flare_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), dy.data_ptr(), lse.data_ptr(),
-            _p(dq), _p(dk), _p(dv), strides, _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _p(y_low), dy.data_ptr(),
+            lse.data_ptr(), _p(dq), _p(dk), _p(dv), strides, _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s,
             1 if causal else 0, ws.data_ptr(), ws.numel(), _raw_stream(index))
     if st:
         _lib.check(st, "flare_attn_bwd")
@@ -323,19 +339,20 @@ class AttnFunction(torch.autograd.Function):
     def forward(ctx, q, k, v, scale, causal, q_lens, k_lens):
         if not any(ctx.needs_input_grad):
             return attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens)
-        y, lse = attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens, save=True)
-        ctx.save_for_backward(q, k, v, y, lse, q_lens, k_lens)
+        y, lse, low = attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens,
+                               save_low=True)
+        ctx.save_for_backward(q, k, v, y, lse, low, q_lens, k_lens)
         ctx.scale, ctx.causal = scale, causal
         return y
 
     @staticmethod
     @_once
     def backward(ctx, dy):
-        q, k, v, y, lse, q_lens, k_lens = ctx.saved_tensors
+        q, k, v, y, lse, low, q_lens, k_lens = ctx.saved_tensors
         need = ctx.needs_input_grad
         dq, dk, dv = attn_bwd(q, k, v, y, _grad_view(dy), lse, ctx.scale, causal=ctx.causal,
                               q_lens=q_lens, k_lens=k_lens, need_dq=need[0],
-                              need_dkv=need[1] or need[2])
+                              need_dkv=need[1] or need[2], y_low=low)
         return dq, dk, dv, None, None, None, None
 
 

@@ -196,16 +196,23 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  T* y = (T*)A.Y + b * A.y.sb + h * A.y.sh + i * A.y.sn + lane * E;
+  const int64_t col = b * A.y.sb + h * A.y.sh + i * A.y.sn + lane * E;
+  T* y = (T*)A.Y + col;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (lane * E + e < A.D) put<T>(y + e, l != 0.f ? acc[e] * inv : 0.f);
+  for (int e = 0; e < E; ++e) {
+    if (lane * E + e >= A.D) continue;
+    const float v = l != 0.f ? acc[e] * inv : 0.f;
+    put<T>(y + e, v);
+    if (sizeof(T) == 2 && A.Ylow) put<T>((T*)A.Ylow + col + e, v - to_f(y[e]));
+  }
   if (A.lse && lane == 0) A.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Backward, before the products: per query row -lse in log2 units (-inf for
 // a row without weight, so that its P is exactly 0) and
-// delta = sum_d dY Y (= sum_j P dP, the softmax's Jacobian term).
+// delta = sum_d dY Y (= sum_j P dP, the softmax's Jacobian term).  Y rounded to
+// bf16 would put an error of 2^-8 of its terms into every dS of the row; with
+// the remainder of that rounding (Ylow) it is 2^-16.
 // LP lanes per row of 16-byte loads; bound by reading Y and dY once.
 template <typename T, int LP>
 __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __grid_constant__ AttnBwdArgs A) {
@@ -224,18 +231,23 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __grid_constan
   if (in && A.q_lens) live = i < A.q_lens[b];
   float s = 0.f;
   if (live && sub * V < A.D) {
-    const uint4 y = *reinterpret_cast<const uint4*>((const T*)A.Y + b * A.y.sb + h * A.y.sh +
-                                                    i * A.y.sn + sub * V);
+    const int64_t at_y = b * A.y.sb + h * A.y.sh + i * A.y.sn + sub * V;
+    const uint4 y = *reinterpret_cast<const uint4*>((const T*)A.Y + at_y);
+    uint4 low = make_uint4(0, 0, 0, 0);
+    if (sizeof(T) == 2 && A.Ylow) low = *reinterpret_cast<const uint4*>((const T*)A.Ylow + at_y);
     const uint4 g = *reinterpret_cast<const uint4*>((const T*)A.dY + b * A.dy.sb + h * A.dy.sh +
                                                     i * A.dy.sn + sub * V);
     const uint32_t yy[4] = {y.x, y.y, y.z, y.w}, gg[4] = {g.x, g.y, g.z, g.w};
+    const uint32_t ll[4] = {low.x, low.y, low.z, low.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (sizeof(T) == 4) {
         s += __uint_as_float(yy[k]) * __uint_as_float(gg[k]);
       } else {
-        s += __uint_as_float(yy[k] << 16) * __uint_as_float(gg[k] << 16);
-        s += __uint_as_float(yy[k] & 0xffff0000u) * __uint_as_float(gg[k] & 0xffff0000u);
+        s += (__uint_as_float(yy[k] << 16) + __uint_as_float(ll[k] << 16)) *
+             __uint_as_float(gg[k] << 16);
+        s += (__uint_as_float(yy[k] & 0xffff0000u) + __uint_as_float(ll[k] & 0xffff0000u)) *
+             __uint_as_float(gg[k] & 0xffff0000u);
       }
     }
   }
@@ -456,13 +468,14 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
                               const flare_strides_t* strides, const int32_t* q_lens,
                               const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
                               int64_t Nk, int64_t D, flare_dtype_t dt, float scale, int causal,
-                              float* lse_save, void* workspace, size_t workspace_bytes,
-                              void* stream) {
+                              float* lse_save, void* y_low_save, void* workspace,
+                              size_t workspace_bytes, void* stream) {
   FLARE_TRY(sizes(B, Hq, Hk, Nq, Nk, D, dt));
   if (!std::isfinite(scale) || !(scale > 0.f)) return FLARE_ERR_INVALID_ARG;
   const void* must[4] = {Q, K, V, Y};
   for (const void* p : must) FLARE_TRY(check_ptr(p));
   if (lse_save) FLARE_TRY(check_ptr(lse_save));
+  if (y_low_save) FLARE_TRY(check_ptr(y_low_save));
   FLARE_TRY(lens(q_lens));
   FLARE_TRY(lens(k_lens));
   AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, causal);
@@ -488,6 +501,7 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   a.q_lens = q_lens, a.k_lens = k_lens;
   a.q = d.q, a.k = d.k, a.v = d.v, a.y = d.y;
   a.Y = Y;
+  a.Ylow = dt == FLARE_BF16 ? y_low_save : nullptr;
   a.lse = lse_save;
   a.part_ml = (float2*)(ws + w.part_ml);
   a.part_o = (float*)(ws + w.part_o);
@@ -500,7 +514,7 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
 }
 
 flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
-                              const void* dY, const float* lse, void* dQ, void* dK, void* dV,
+                              const void* y_low, const void* dY, const float* lse, void* dQ, void* dK, void* dV,
                               const flare_strides_t* strides, const int32_t* q_lens,
                               const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
                               int64_t Nk, int64_t D, flare_dtype_t dt, float scale, int causal,
@@ -512,6 +526,7 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
     return FLARE_ERR_INVALID_ARG;
   const void* must[9] = {Q,   K, V, Y, dY, lse, dQ ? dQ : dK, dK ? dK : dQ, dV ? dV : dQ};
   for (const void* p : must) FLARE_TRY(check_ptr(p));
+  if (y_low) FLARE_TRY(check_ptr(y_low));
   FLARE_TRY(lens(q_lens));
   FLARE_TRY(lens(k_lens));
   AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, causal);
@@ -543,6 +558,7 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   a.q_lens = q_lens, a.k_lens = k_lens;
   a.q = d.q, a.k = d.k, a.v = d.v, a.y = d.y, a.dy = d.dy, a.dq = d.dq, a.dk = d.dk, a.dv = d.dv;
   a.Q = Q, a.K = K, a.V = V, a.Y = Y, a.dY = dY, a.lse = lse;
+  a.Ylow = dt == FLARE_BF16 ? y_low : nullptr;
   a.dQ = dQ, a.dK = dK, a.dV = dV;
   a.nl = (float*)(ws + w.stats);
   a.delta = a.nl + B * Hq * Nq;

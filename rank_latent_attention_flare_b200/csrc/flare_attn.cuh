@@ -129,7 +129,7 @@ struct AttnFwdArgs {
   float c;                 // scale * log2(e)
   const int32_t *q_lens, *k_lens;
   Tok q, k, v, y;
-  void* Y;
+  void *Y, *Ylow;          // Ylow: what rounding Y left over, may be NULL
   float* lse;              // may be NULL
   float2* part_ml;         // [units * splits][rows] (reference, sum), log2 units
   float* part_o;           // [units * splits][rows][DP]
@@ -144,7 +144,7 @@ struct AttnBwdArgs {
   float scale, c;
   const int32_t *q_lens, *k_lens;
   Tok q, k, v, y, dy, dq, dk, dv;
-  const void *Q, *K, *V, *Y, *dY;
+  const void *Q, *K, *V, *Y, *Ylow, *dY;   // Ylow may be NULL
   const float* lse;
   void *dQ, *dK, *dV;
   float *nl, *delta;       // [B*Hq][Nq]: -lse in log2 units (-inf: no weight), sum(dY * Y)

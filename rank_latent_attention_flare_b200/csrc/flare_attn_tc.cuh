@@ -166,18 +166,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 
 // Writes 32 consecutive fp32 values times f as bf16 to p[0..32), the columns
-// below D only (D and col0 are multiples of 8, rows 16-byte aligned).
+// below D only (D and col0 are multiples of 8, rows 16-byte aligned); with
+// `low` also what the rounding left over, rounded to bf16.
 __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* p, const uint32_t (&o)[32], float f,
-                                              int col0, int D) {
+                                              int col0, int D, __nv_bfloat16* low = nullptr) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     if (col0 + 8 * g >= D) break;
-    uint4 v;
-    v.x = pack_bf16(__uint_as_float(o[8 * g]) * f, __uint_as_float(o[8 * g + 1]) * f);
-    v.y = pack_bf16(__uint_as_float(o[8 * g + 2]) * f, __uint_as_float(o[8 * g + 3]) * f);
-    v.z = pack_bf16(__uint_as_float(o[8 * g + 4]) * f, __uint_as_float(o[8 * g + 5]) * f);
-    v.w = pack_bf16(__uint_as_float(o[8 * g + 6]) * f, __uint_as_float(o[8 * g + 7]) * f);
-    *reinterpret_cast<uint4*>(p + 8 * g) = v;
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = pack_bf16(__uint_as_float(o[8 * g + 2 * k]) * f, __uint_as_float(o[8 * g + 2 * k + 1]) * f);
+    *reinterpret_cast<uint4*>(p + 8 * g) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (low == nullptr) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = pack_bf16(fmaf(__uint_as_float(o[8 * g + 2 * k]), f, -bf_lo(v[k])),
+                       fmaf(__uint_as_float(o[8 * g + 2 * k + 1]), f, -bf_hi(v[k])));
+    *reinterpret_cast<uint4*>(low + 8 * g) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 

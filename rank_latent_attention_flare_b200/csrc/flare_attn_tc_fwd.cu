@@ -522,7 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (QT == 2 || w == 0) {
       const float inv = some ? 1.f / l : 0.f;
-      __nv_bfloat16* y = (__nv_bfloat16*)A.Y + b * A.y.sb + h * A.y.sh + i * A.y.sn;
+      const int64_t at = b * A.y.sb + h * A.y.sh + i * A.y.sn;
+      __nv_bfloat16* y = (__nv_bfloat16*)A.Y + at;
+      __nv_bfloat16* low = A.Ylow ? (__nv_bfloat16*)A.Ylow + at : nullptr;
 #pragma unroll 1
       for (int k = 0; k < DP / 32; ++k) {
         uint32_t o[32];
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             o[x] = some ? __float_as_uint(v) : 0u;   // also clears rows never computed
           }
-          store_bf16x32(y + 32 * k, o, inv, 32 * k, A.D);
+          store_bf16x32(y + 32 * k, o, inv, 32 * k, A.D, low ? low + 32 * k : nullptr);
         }
         __syncwarp();   // the warp's lanes load together
       }

@@ -62,8 +62,9 @@ class Attn:
         self.r = 0.0 if self.dt == torch.float32 else U[self.dt]
         self.D = D
         self.yabs = self.p @ self.v.abs()
-        self.y_bound = (self.r + 2 * self.e_p + (Nk + 1) * S) * self.yabs + \
-            U[self.dt] * self.y.abs() + 1e-30
+        # before the output's rounding, and with it
+        self.y_pure = (self.r + 2 * self.e_p + (Nk + 1) * S) * self.yabs + 1e-30
+        self.y_bound = self.y_pure + U[self.dt] * self.y.abs()
         self.lse_bound = self.e_p + 2.0 ** -22 * torch.where(torch.isinf(self.lse), 0.0,
                                                              self.lse.abs()) + 1e-6
 
@@ -77,8 +78,9 @@ class Attn:
         B, H, N, D = t.shape
         return t.view(B, H // self.G, self.G, N, D).sum(2)
 
-    def grads(self, dy):
-        """(dq, dk, dv), their bounds."""
+    def grads(self, dy, low=False):
+        """(dq, dk, dv), their bounds; ``low``: delta comes from y and the
+        remainder of its rounding, which is off by 2^-16 of y."""
         dy = self.clean(dy, self.mq)
         p, s, r, u = self.p, self.s, self.r, U[self.dt]
         dp = dy @ self.v.transpose(-1, -2)
@@ -88,8 +90,9 @@ class Attn:
         dq = s * ds @ self.k
         dk = self._heads(s * ds.transpose(-1, -2) @ self.q)
         # dP and delta are float32 sums of D terms; delta sees the rounded y
+        e_y = self.y_pure + U[self.dt] ** 2 * self.y.abs() if low else self.y_bound
         e_dp = (self.D + 1) * S * (dy.abs() @ self.v.abs().transpose(-1, -2))
-        e_delta = (dy.abs() * (self.y_bound + (self.D + 1) * S * self.y.abs())).sum(-1, keepdim=True)
+        e_delta = (dy.abs() * (e_y + (self.D + 1) * S * self.y.abs())).sum(-1, keepdim=True)
         e_ds = (r + self.e_p + 4 * S) * ds.abs() + 2 * p * (e_dp + e_delta)
         nq, nk = (self.nq * self.G + 1) * S, (self.n + 1) * S
         t = ds.abs() + e_ds

@@ -30,19 +30,19 @@ def strides(*triples):
 
 
 def attn_fwd(lib, B=2, Hq=4, Hk=2, Nq=30, Nk=50, D=64, dt=1, scale=0.125, q=F, k=F, v=F, y=F,
-             st=None, ql=None, kl=None, lse=None, ws=F, wsb=None):
+             st=None, ql=None, kl=None, lse=None, low=None, ws=F, wsb=None):
     if wsb is None:
         wsb = lib.flare_attn_workspace_size(0, B, Hq, Hk, Nq, Nk, D, dt) or (1 << 30)
-    return lib.flare_attn_fwd(q, k, v, y, st, ql, kl, B, Hq, Hk, Nq, Nk, D, dt, scale, 0, lse, ws,
-                              wsb, None)
+    return lib.flare_attn_fwd(q, k, v, y, st, ql, kl, B, Hq, Hk, Nq, Nk, D, dt, scale, 0, lse,
+                              low, ws, wsb, None)
 
 
 def attn_bwd(lib, B=2, Hq=4, Hk=2, Nq=30, Nk=50, D=64, dt=1, scale=0.125, lse=F, dq=F, dk=F, dv=F,
-             st=None, ws=F, wsb=None):
+             low=None, st=None, ws=F, wsb=None):
     if wsb is None:
         wsb = lib.flare_attn_workspace_size(1, B, Hq, Hk, Nq, Nk, D, dt) or (1 << 30)
-    return lib.flare_attn_bwd(F, F, F, F, F, lse, dq, dk, dv, st, None, None, B, Hq, Hk, Nq, Nk, D,
-                              dt, scale, 0, ws, wsb, None)
+    return lib.flare_attn_bwd(F, F, F, F, low, F, lse, dq, dk, dv, st, None, None, B, Hq, Hk, Nq,
+                              Nk, D, dt, scale, 0, ws, wsb, None)
 
 
 @no_gpu_only
@@ -64,7 +64,9 @@ def test_attn_pointers_and_workspace(lib):
     for name in ("q", "k", "v", "y"):
         assert attn_fwd(lib, **{name: None}) == INVALID
         assert attn_fwd(lib, **{name: F + 8}) == INVALID
-    assert attn_fwd(lib, lse=F + 4) == INVALID
+    assert attn_fwd(lib, lse=F + 4) == INVALID and attn_fwd(lib, low=F + 2) == INVALID
+    assert attn_fwd(lib, low=F) == CUDA and attn_bwd(lib, low=F) == CUDA
+    assert attn_bwd(lib, low=F + 8) == INVALID
     assert attn_fwd(lib, ql=F + 2) == INVALID and attn_fwd(lib, kl=F + 1) == INVALID
     assert attn_fwd(lib, ql=F + 4, kl=F + 8) == CUDA
     assert attn_bwd(lib, lse=None) == INVALID

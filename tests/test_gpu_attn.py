@@ -45,9 +45,14 @@ def check(q, k, v, dy, causal=False, q_lens=None, k_lens=None, scale=None, backw
     Hk, Nk = k.shape[1], k.shape[2]
     ws = torch.empty(fl.attn_workspace_size(False, B, Hq, Hk, Nq, Nk, D, q.dtype),
                      dtype=torch.uint8, device=DEV)
-    y, lse = fl.attn_fwd(q, k, v, scale, save=True, workspace=ws, **kw)
+    y, lse, low = fl.attn_fwd(q, k, v, scale, save_low=True, workspace=ws, **kw)
     assert fl.device_status(ws) == 0
     within(y, ref.y, ref.y_bound, "y")
+    if low is None:
+        assert q.dtype == F32
+    else:   # y and its remainder together are as good as before the rounding
+        within(y.double() + low.double(), ref.y, ref.y_pure + 2.0 ** -16 * ref.y.abs(), "y + low")
+        poison(low, q_lens)
     empty = torch.isinf(ref.lse)
     assert torch.equal(torch.isinf(lse) & (lse < 0), empty)
     assert not y[empty].any()
@@ -55,15 +60,15 @@ def check(q, k, v, dy, causal=False, q_lens=None, k_lens=None, scale=None, backw
     assert (err <= ref.lse_bound).all()
     if not backward:
         return
-    y = torch.where(empty.unsqueeze(-1), 0.0, y.float()).to(y.dtype)
     poison(y, q_lens)   # y and dy are not read past the lengths
     ws = torch.empty(fl.attn_workspace_size(True, B, Hq, Hk, Nq, Nk, D, q.dtype),
                      dtype=torch.uint8, device=DEV)
-    got = fl.attn_bwd(q, k, v, y, dy, lse, scale, workspace=ws, **kw)
-    assert fl.device_status(ws) == 0
-    want, bounds = ref.grads(dy)
-    for name, a, b, e in zip(("dq", "dk", "dv"), got, want, bounds):
-        within(a, b, e, name)
+    for rest in (None, low):
+        got = fl.attn_bwd(q, k, v, y, dy, lse, scale, workspace=ws, y_low=rest, **kw)
+        assert fl.device_status(ws) == 0
+        want, bounds = ref.grads(dy, low=rest is not None)
+        for name, a, b, e in zip(("dq", "dk", "dv"), got, want, bounds):
+            within(a, b, e, name)
 
 
 # B, Hq, Hk, Nq, Nk, D, causal, q_lens, k_lens

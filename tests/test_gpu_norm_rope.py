@@ -175,8 +175,10 @@ def test_layer_of_them_together():
     leaves = [qkv, lat, *ws]
     grads = torch.autograd.grad(((full + low) * dy).float().sum(), leaves)
     # by hand, with the library's own calls
-    y, lse = fl.attn_fwd(qo.detach(), ko.detach(), v, q_lens=lens, k_lens=lens, save=True)
-    dqo, dko, dv = fl.attn_bwd(qo.detach(), ko.detach(), v, y, dy, lse, q_lens=lens, k_lens=lens)
+    y, lse, low = fl.attn_fwd(qo.detach(), ko.detach(), v, q_lens=lens, k_lens=lens,
+                              save_low=True)
+    dqo, dko, dv = fl.attn_bwd(qo.detach(), ko.detach(), v, y, dy, lse, q_lens=lens, k_lens=lens,
+                               y_low=low)
     _, Z, l2 = fl.flare_fwd(lat.detach(), ko.detach(), v, save=True, seq_lens=lens)
     dl, dk2, dv2 = fl.flare_bwd(lat.detach(), ko.detach(), v, dy, Z, l2, seq_lens=lens)
     dq, dk, dwq, dwk = fl.qk_norm_rope_bwd(q, k, wq.detach(), wk.detach(), cos, sin, dqo,
