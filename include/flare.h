@@ -566,7 +566,7 @@ FLARE_API flare_status_t flare_eval_exp2(const float* x, float* y, int64_t n, in
  *             FLARE_F32): what rounding Y to bf16 left over, for the backward.
  *   workspace flare_attn_workspace_size(0, ...) bytes, 256-byte aligned.
  *
- * Supported: D a multiple of 8 up to 128; Nq, Nk <= 2^30; B Hq <= 65535;
+ * Supported: D a multiple of 8 up to 128; Nq, Nk <= 2^30; B Hq <= 2^24;
  * scale finite and > 0.  K and V of a key that the mask hides from a query,
  * but that lies within k_lens, have to be finite.  Results do not depend on
  * timing (no atomics).  Enqueued on `stream`.

@@ -370,7 +370,7 @@ flare_status_t sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, 
   if (D % 8 != 0 || D > 128) return FLARE_ERR_UNSUPPORTED;
   // 32-bit token indices (with room for a tile before and after)
   if (Nq > (1LL << 30) || Nk > (1LL << 30)) return FLARE_ERR_UNSUPPORTED;
-  if (B * Hq > 65535) return FLARE_ERR_UNSUPPORTED;
+  if (B * Hq > (1LL << 24)) return FLARE_ERR_UNSUPPORTED;
   if ((double)B * Hq * Nq * D >= 1099511627776.0 || (double)B * Hk * Nk * D >= 1099511627776.0)
     return FLARE_ERR_INVALID_ARG;   // 2^40
   return FLARE_OK;

@@ -55,7 +55,8 @@ def test_attn_sizes(lib, call):
         assert call(lib, **bad) == INVALID, bad
     for s in (0.0, -1.0, math.nan, math.inf):
         assert call(lib, scale=s) == INVALID
-    for bad in (dict(D=4), dict(D=20), dict(D=136), dict(Nk=(1 << 30) + 1), dict(B=20000)):
+    for bad in (dict(D=4), dict(D=20), dict(D=136), dict(Nk=(1 << 30) + 1),
+                dict(B=1 << 20, Hq=32)):
         assert call(lib, **bad) == UNSUPPORTED, bad
 
 
@@ -165,3 +166,31 @@ def test_binding_refuses_host_tensors():
 def test_signatures_take_integers(lib):
     assert ctypes.sizeof(ctypes.c_size_t) == 8
     assert lib.flare_attn_workspace_size(0, 1, 1, 1, 1, 1, 8, 0) > 0
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_shapes():
+    """Checks of the binding and of the library that need device tensors."""
+    q, k = torch.zeros(2, 4, 5, 16, device="cuda"), torch.zeros(2, 3, 6, 16, device="cuda")
+    with pytest.raises(ValueError):
+        fl.attn_fwd(q, k, k)                                    # 4 heads over 3
+    k = torch.zeros(2, 2, 6, 16, device="cuda")
+    with pytest.raises(ValueError):
+        fl.attn_fwd(q, k, k[:, :, :5])
+    with pytest.raises(ValueError):
+        fl.attn_fwd(q, k, k.double())
+    with pytest.raises(TypeError):
+        fl.attn_fwd(q.half(), k.half(), k.half())
+    with pytest.raises(ValueError):
+        fl.attn_fwd(q, k, k, k_lens=torch.tensor([6, 6], device="cuda"))   # int64
+    with pytest.raises(fl.FlareError):
+        fl.attn_fwd(q[..., :12], k[..., :12], k[..., :12])
+    with pytest.raises(ValueError):
+        fl.qk_norm_rope_fwd(q, k)                               # 5 and 6 tokens
+    with pytest.raises(ValueError):
+        fl.qk_norm_rope_fwd(q, q, torch.ones(8, device="cuda"))
+    with pytest.raises(ValueError):
+        fl.qk_norm_rope_fwd(q, q, None, None, torch.zeros(5, 8, device="cuda"))
+    with pytest.raises(ValueError):
+        fl.qk_norm_rope_fwd(q, q, None, None, torch.zeros(4, 8, device="cuda"),
+                            torch.zeros(4, 8, device="cuda"))

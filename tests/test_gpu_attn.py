@@ -94,6 +94,10 @@ CASES = {
     "five_shared": (1, 10, 2, 150, 150, 48, True, None, None),
     "split_keys": (1, 2, 1, 33, 9000, 64, False, None, None),
     "split_queries": (1, 4, 1, 3000, 40, 128, False, None, None),
+    # more key tiles than SMs, one or a few query tiles each
+    "latents": (2, 4, 4, 100, 9000, 64, False, None, [9000, 4097]),
+    "latents_shared": (3, 8, 2, 130, 7000, 32, False, [130, 0, 128], [1, 7000, 6500]),
+    "window_of_keys": (2, 4, 2, 200, 9000, 64, True, [200, 77], [8999, 150]),
 }
 
 
@@ -113,6 +117,32 @@ def test_scale_and_large_logits(dt):
     k *= torch.linspace(0.1, 3.0, 1000, device=DEV).view(1, 1, -1, 1).to(dt)
     check(q, k, v, dy, scale=0.5)
     check(q, -k, v, dy, causal=True, scale=0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads(D):
+    """More batch elements times heads than a grid has rows, one token each."""
+    q, k, v, dy = tensors(BF, 1100, 64, 8, 1, 20, D, seed=20)
+    check(q, k, v, dy, causal=True, k_lens=[1 + i % 20 for i in range(1100)])
+
+
+def test_second_derivative_is_refused():
+    q, k, v, dy = (t.requires_grad_() for t in tensors(F32, 1, 1, 1, 8, 8, 32, seed=21))
+    (dq,) = torch.autograd.grad(fl.attn(q, k, v), q, dy, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dq.sum(), k)
+
+
+def test_key_gradients_alone():
+    """A frozen query, a frozen cache: only what needs a gradient gets one."""
+    q, k, v, dy = tensors(BF, 2, 4, 2, 70, 200, 64, seed=22)
+    ref = Attn(q, k, v)
+    want, bounds = ref.grads(dy, low=True)
+    for which in ((0,), (1,), (2,), (1, 2)):
+        leaves = [t.detach().requires_grad_(i in which) for i, t in enumerate((q, k, v))]
+        got = torch.autograd.grad(fl.attn(*leaves), [leaves[i] for i in which], dy)
+        for g, i in zip(got, which):
+            within(g, want[i], bounds[i], "qkv"[i])
 
 
 @pytest.mark.parametrize("dt", [F32, BF], ids=["fp32", "bf16"])
