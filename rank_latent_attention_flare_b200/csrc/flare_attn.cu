@@ -16,7 +16,7 @@ namespace {
 // causal mask their sizes spread evenly up to `tiles`, longest first: the
 // places share the sum, and a piece at the end leaves some of them idle.
 int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double setup, double join,
-                  double part) {
+                  double part, double* estimate = nullptr) {
   int best = 1;
   double best_cost = 1e300;
   const int64_t hi = imin64(tiles, imax64(1, 4LL * slots / imax64(units, 1)));
@@ -35,6 +35,7 @@ int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double s
       best = (int)s;
     }
   }
+  if (estimate) *estimate = best_cost;
   return best;
 }
 
@@ -50,20 +51,33 @@ AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
     for (int64_t g = 2; g <= G; ++g)
       if (G % g == 0 && g * d.Nq <= tile) p.hpt = (int)g;
   const int64_t rows = p.hpt > 1 ? p.hpt * d.Nq : d.Nq;
-  p.qt = tc && rows > kAttnTile ? 2 : 1;
-  p.rows = (int)(tile * p.qt);
-  p.qblocks = (rows + p.rows - 1) / p.rows;
-  p.units = d.B * (d.Hq / p.hpt) * p.qblocks;
   const int64_t ktiles = (d.Nk + tile - 1) / tile;
   // one or a few tokens see about all keys
   const bool triangle = d.causal && 2 * d.Nq > d.Nk;
-  // a part's rows x DP floats at an SM's share of the memory bandwidth (5500
-  // written and read back in a microsecond), against 2.0 us (two query tiles),
-  // 1.0 us (one) or 8 us for a tile (CUDA cores: two CTAs share an SM)
-  const double part =
-      (double)imin64(rows, p.rows) * attn_dp(d.D) / (tc ? 5500.0 * p.qt : 22000.0);
-  p.splits = tc ? choose_splits(p.units, ktiles, sms, triangle, p.qt == 2 ? 2.0 : 4.0, 3.0, part)
-                : choose_splits(p.units, ktiles, 2 * sms, triangle, 0.5, 0.5, part);
+  // One or two query tiles a CTA: two read each key tile once for both and run
+  // at 1.06 times the rate (16 heads of 4096: 129 against 137 us at D 128, 111
+  // against 119 at D 64); one leaves no half empty (2 x 16 heads of 333 queries
+  // over 5001 keys, D 64: 42 against 48 us).  Times in microseconds: a tile 2.0
+  // (two), 1.06 (one) or 8 (CUDA cores, two CTAs an SM), a CTA's start and end
+  // about 4, a part's rows x DP floats at an SM's share of the memory bandwidth
+  // (5500 written and read back in a microsecond).
+  double best = 1e300;
+  for (int qt = 1; qt <= (tc && rows > kAttnTile ? 2 : 1); ++qt) {
+    AttnPlan c = p;
+    c.qt = qt;
+    c.rows = (int)(tile * qt);
+    c.qblocks = (rows + c.rows - 1) / c.rows;
+    c.units = d.B * (d.Hq / c.hpt) * c.qblocks;
+    const double us = tc ? (qt == 2 ? 2.0 : 1.06) : 8.0;
+    const double part = (double)imin64(rows, c.rows) * attn_dp(d.D) / 5500.0;
+    double cost;
+    c.splits = choose_splits(c.units, ktiles, tc ? sms : 2 * sms, triangle, 4.0 / us, 3.0 / us,
+                             (tc ? part : 2 * part) / us, &cost);
+    if (cost * us < best) {
+      best = cost * us;
+      p = c;
+    }
+  }
   return p;
 }
 

@@ -19,9 +19,8 @@
 //
 // TMEM: S of warpgroup w at columns 128 w, O at 256 + DP w.  P replaces the
 // first half of S: its first 64 keys are handed to the tensor core while the
-// others are computed, and S of the next tile follows the product.  With two
-// query tiles and D <= 64 there is room for P at 384 + 64 w: S of the next
-// tile is then computed as soon as the softmax has read S, so that the
+// others are computed, and S of the next tile follows the product.  For
+// D <= 64 there is room for P at 384 + 64 w: S of the next tile is then computed as soon as the softmax has read S, so that the
 // softmax does not wait for the tensor core (D = 64, 16 heads of 4096
 // tokens, all pairs: 113 us instead of 123).  All MMAs are issued by one thread, in batches whose
 // length is a compile-time constant (KS steps over D): a product under a
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = FwdLayout<DP, QT>;
   using T = Tile<DP>;
   constexpr int NS = L::STAGES;
-  constexpr bool APART = QT == 2 && DP <= 64;   // P apart from S
+  constexpr bool APART = DP <= 64;   // P apart from S
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&kv_empty[item_k<QT>(0) % NS]);
           }
         }
-        if (APART) {
+        if (APART && QT == 2) {
           // the warpgroups run half a tile apart: S0, then the other's product,
           // S1, then this one's product
           auto next_S = [&](int w, int j) -> bool {
@@ -308,16 +307,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_S(j, j);
             mma_commit(&kv_empty[item_k<QT>(j) % NS]);
           }
-          for (int j = 0; ok && j < n; ++j) {
-            const int w = j & 1;
-            if (!(ok = full(item_v<QT>(j)) && do_PV(w, j, j >> 1))) break;
+          // S of tile j + 2 once S of tile j is read (P apart) or behind its product
+          auto next_S = [&](int j) -> bool {
+            if (j + 2 >= n) return true;
+            if (!full(item_k<QT>(j + 2))) return false;
+            if (APART && !mbar_wait(&early[j & 1], (uint32_t)((j >> 1) & 1))) return false;
+            tc_fence_after();
+            issue_S(j & 1, j + 2);
+            mma_commit(&kv_empty[item_k<QT>(j + 2) % NS]);
+            return true;
+          };
+          auto next_PV = [&](int j) -> bool {
+            if (!full(item_v<QT>(j)) || !do_PV(j & 1, j, j >> 1)) return false;
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
-            if (j + 2 < n) {
-              if (!(ok = full(item_k<QT>(j + 2)))) break;
-              tc_fence_after();
-              issue_S(w, j + 2);
-              mma_commit(&kv_empty[item_k<QT>(j + 2) % NS]);
-            }
+            return true;
+          };
+          for (int j = 0; ok && j < n + APART; ++j) {
+            if (APART) ok = next_S(j) && (j == 0 || next_PV(j - 1));
+            else ok = next_PV(j) && next_S(j);
             if (*abort_flag) ok = false;
           }
         }
