@@ -1,4 +1,5 @@
-"""FLARE / FLARE++ low-rank attention routing on B200 (sm_100a).
+"""FLARE / FLARE++ low-rank attention routing on B200 (sm_100a), and the
+softmax attention, norms and rotation beside it.
 
 The compute lives in ``libflare.so`` (hand-written CUDA: tcgen05/TMEM/TMA
 tensor-core kernels and CUDA-core kernels) behind the C ABI declared in

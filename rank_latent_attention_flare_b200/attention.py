@@ -22,8 +22,9 @@ from ._lib import FlareError
 _f = importlib.import_module(__package__ + ".flare")
 
 
-# the current stream's handle by device index
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current stream's handle by device index (the short way where torch has it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _NoSwitch:

@@ -510,7 +510,6 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   AttnFwdArgs a = {};
   a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk), a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
   a.hpt = p.hpt, a.qblocks = (int)p.qblocks, a.splits = p.splits, a.causal = d.causal;
-  a.units = p.units;
   a.c = scale * kLog2e;
   a.q_lens = q_lens, a.k_lens = k_lens;
   a.q = d.q, a.k = d.k, a.v = d.v, a.y = d.y;

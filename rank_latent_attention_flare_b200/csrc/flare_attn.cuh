@@ -78,9 +78,9 @@ inline int attn_ks(int64_t D) { return D <= 32 ? 2 : D <= 64 ? 4 : D <= 80 ? 5 :
 inline bool attn_tc(flare_dtype_t dt) { return dt == FLARE_BF16; }
 
 // How the forward is cut.  A CTA takes `qt` tiles of query rows (tensor
-// cores: 128 rows each; CUDA cores: one tile of 64) of one head, or, when
+// cores: one or two of 128 rows; CUDA cores: one of 64) of one head, or, when
 // few queries leave a tile mostly empty, the queries of `hpt` heads that
-// share a key head (row = head * Nq + query), and one of `splits` equal
+// share a key head (row = head * Nq + query), and one of `splits` near-equal
 // parts of the key tiles it sees.
 struct AttnPlan {
   int qt = 1, hpt = 1, rows = 0, splits = 1;
@@ -125,7 +125,6 @@ __device__ __forceinline__ void attn_check_lens(const int32_t* q_lens, const int
 struct AttnFwdArgs {
   int B, Hq, Hk, G, Nq, Nk, D;   // G = Hq / Hk
   int hpt, qblocks, splits, causal;
-  int64_t units;
   float c;                 // scale * log2(e)
   const int32_t *q_lens, *k_lens;
   Tok q, k, v, y;
