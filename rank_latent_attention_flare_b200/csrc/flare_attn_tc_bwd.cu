@@ -549,10 +549,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // columns below cl do not see this lane's key
         const int cl = it.sq.causal ? it.krow0 + r - it.sq.off - row0 - kCols * w : -1;
         const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
-        if (!warp_all(mbar_wait(&nl_full[s], (uint32_t)((J / NB) & 1)))) {
-          ok = false;
-          break;
-        }
+        ok &= mbar_wait(&nl_full[s], (uint32_t)((J / NB) & 1));
         float nv[kCols];   // read ahead of the wait for S
 #pragma unroll
         for (int x = 0; x < kCols; x += 4) {
@@ -560,10 +557,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           nv[x] = v.x, nv[x + 1] = v.y, nv[x + 2] = v.z, nv[x + 3] = v.w;
         }
         const bool gone = nl[lane] == -INFINITY;
-        if (!warp_all(mbar_wait(&s_full[J % SB], (uint32_t)((J / SB) & 1)))) {
-          ok = false;
-          break;
-        }
+        ok &= mbar_wait(&s_full[J % SB], (uint32_t)((J / SB) & 1));
         __syncwarp();
         tc_fence_after();
         uint32_t p[kCols];
@@ -581,10 +575,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&p_ready[J % SB]);
-        if (!warp_all(mbar_wait(dp_full, (uint32_t)(J & 1)))) {
-          ok = false;
-          break;
-        }
+        ok &= mbar_wait(dp_full, (uint32_t)(J & 1));
         __syncwarp();
         tc_fence_after();
         uint32_t g[kCols];
@@ -596,6 +587,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(ds_ready);
+        if (!(ok = warp_all(ok))) break;   // a wait ran out: one vote for the three
       }
       if (!ok || !(ok = warp_all(mbar_wait(done, (uint32_t)(c & 1))))) break;
       __syncwarp();
@@ -829,10 +821,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const int row0 = tile_row0(t, kAttnTile, sq.kl);
       const int cl = t * kAttnTile - row0 - kCols * w;
       const int ch = (sq.causal ? i + sq.off - row0 : 127) - kCols * w;
-      if (!warp_all(mbar_wait(&s_full[j & 1], (uint32_t)((j >> 1) & 1)))) {
-        ok = false;
-        break;
-      }
+      ok &= mbar_wait(&s_full[j & 1], (uint32_t)((j >> 1) & 1));
       __syncwarp();
       tc_fence_after();
       uint32_t p[kCols];
@@ -844,10 +833,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       } else {
         exp_cols<false, kBwdPoly>(p, A.c, nl, none);
       }
-      if (!warp_all(mbar_wait(dp_full, (uint32_t)(j & 1)))) {
-        ok = false;
-        break;
-      }
+      ok &= mbar_wait(dp_full, (uint32_t)(j & 1));
       __syncwarp();
       tc_fence_after();
       uint32_t g[kCols];
@@ -858,6 +844,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(ds_ready);
+      if (!(ok = warp_all(ok))) break;   // a wait ran out: one vote for both
     }
     if (ok && n > 0 && !warp_all(mbar_wait(done, 0))) ok = false;
     if (!ok) {
