@@ -140,6 +140,7 @@ struct AttnBwdArgs {
   int B, Hq, Hk, G, Nq, Nk, D;   // G = Hq / Hk
   int tile, ktiles, qtiles, dkv_splits, dq_splits, causal;
   int64_t dkv_units, dq_units;
+  int dkv_ctas;            // tensor-core kernel: the first CTAs are dK's and dV's
   float scale, c;
   const int32_t *q_lens, *k_lens;
   Tok q, k, v, y, dy, dq, dk, dv;

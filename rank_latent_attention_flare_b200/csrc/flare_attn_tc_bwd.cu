@@ -1,10 +1,10 @@
 // Tensor-core backward of softmax attention for sm_100a (bf16, D up to 128):
-// two kernels that recompute the probabilities, one over key tiles (dK, dV),
-// one over query tiles (dQ).  Each sum stays in one CTA's TMEM, so nothing is
+// a kernel that recomputes the probabilities twice, in CTAs over key tiles (dK,
+// dV) and CTAs over query tiles (dQ).  Each sum stays in one CTA's TMEM, so nothing is
 // added by atomics and results repeat bit by bit; the price is computing the
 // logits and dP twice, 7 products per tile pair instead of 5.
 //
-// dK, dV (attn_dkv_kernel): TMEM lanes are keys, columns queries.  Per tile
+// dK, dV (attn_dkv): TMEM lanes are keys, columns queries.  Per tile
 // of 128 queries of each head that shares the keys:
 //   S^T = K Q^T,  P^T = 2^(c S^T + nl),   dV += P^T dY     (P^T from TMEM)
 //   dP^T = V dY^T, dS^T = P^T (dP^T - delta), dK += dS^T Q
@@ -15,7 +15,7 @@
 // products to run: {dV_j, S_j+1} while dS_j is computed, {dK_j, dP_j+1}
 // while P_j+1 is.
 //
-// dQ (attn_dq_kernel): lanes are queries, columns keys, nl and delta one per
+// dQ (attn_dq): lanes are queries, columns keys, nl and delta one per
 // lane:  S = Q K^T, dP = dY V^T, dS = P (dP - delta), dQ += dS K.  S has two
 // buffers, so that P_j+1 is computed while {dQ_j, dP_j+1} run.
 //
@@ -42,6 +42,10 @@ constexpr int kBwdPoly = 3;
 constexpr int kBThreads = 640;
 constexpr int kBWarpTma = 16, kBWarpMma = 17, kBWarpAux = 18;
 constexpr int kCols = 32;
+// 512 x 104 + 128 x 64 = 640 x 96; without the split the softmax's loop spills
+// (2 x 8 heads of 6000, D 64: 567 against 540 us)
+constexpr int kBRegsSoftmax = 104;
+constexpr int kBRegsProducer = 64;
 
 // 2^(c a + n) for a lane's columns, in place, n per column or one for all:
 // probabilities in float32.
@@ -139,7 +143,7 @@ template <int DP>
 struct DkvLayout {
   using T = Tile<DP>;
   // ring of Q and dY tiles in the order Q0 dY0 Q1 dY1 ...
-  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 8 : 12;
+  static constexpr int SLOTS = DP == 128 ? 5 : 8;
   static constexpr int KB = DP == 128 ? 1 : 2;   // buffers of K and V
   static constexpr int NB = 2;                   // buffers of (nl, delta)
   static constexpr int K_OFF = 0;                // [KB][K, V]
@@ -190,15 +194,16 @@ static_assert(sizeof(DkvItem) <= 64, "a slot of the ring of pieces");
 // The pieces of a CTA: one in each round of the grid, the order turned round
 // every other time, so that sorted pieces add up to about the same.
 struct Rounds {
-  unsigned total, base;   // total < 2^31
+  unsigned total, ctas, base;   // total < 2^31
   bool back;
-  __device__ __forceinline__ explicit Rounds(unsigned total_) : total(total_), base(0), back(false) {}
+  __device__ __forceinline__ Rounds(unsigned total_, unsigned ctas_)
+      : total(total_), ctas(ctas_), base(0), back(false) {}
   __device__ __forceinline__ bool more() const { return base < total; }
   __device__ __forceinline__ unsigned index() const {
-    return base + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return base + (back ? ctas - 1 - blockIdx.x : blockIdx.x);
   }
   __device__ __forceinline__ void next() {
-    base += gridDim.x;
+    base += ctas;
     back = !back;
   }
 };
@@ -249,12 +254,9 @@ struct Cursor {
 // between the tiles.  Long pieces are better left to the hardware, one CTA
 // each: it hands them out as SMs become free.
 template <int KS>
-__global__ void __launch_bounds__(kBThreads, 1)
-    attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-                    const __grid_constant__ AttnBwdArgs A) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void attn_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                         const CUtensorMap& tmV, const CUtensorMap& tmG,
+                                         const AttnBwdArgs& A) {
   constexpr int DP = attn_dp(16 * KS);
   using L = DkvLayout<DP>;
   using T = Tile<DP>;
@@ -314,222 +316,226 @@ __global__ void __launch_bounds__(kBThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kBWarpTma) {
-    // --------------------------------------------------------------- TMA
-    if (elect_one()) {
-      bool ok = true;
-      int c = 0, it = 0;   // pieces and ring items so far
-      for (Rounds rd(total); ok && rd.more(); rd.next()) {
-        if (rd.index() >= total) continue;
-        const DkvItem w(A, rd.index());
-        if (w.n == 0) continue;
-        const int kb = (A.bcast & 2) ? 0 : w.b, kh = (A.bcast & 16) ? 0 : w.hk;
-        const int vb = (A.bcast & 4) ? 0 : w.b, vh = (A.bcast & 32) ? 0 : w.hk;
-        const int qb = (A.bcast & 1) ? 0 : w.b, gb = (A.bcast & 64) ? 0 : w.b;
-        const int kvb = c % KB, used = c / KB;
-        if (used > 0 && !(ok = mbar_wait(&kv_empty[kvb], (uint32_t)((used - 1) & 1)))) break;
-        uint8_t* kv = smem + L::K_OFF + kvb * 2 * T::BYTES;
-        mbar_arrive_expect_tx(&kv_full[kvb], 2 * T::BYTES);
-        load_tile<DP>(kv, &tmK, &kv_full[kvb], w.krow0, kh, kb);
-        load_tile<DP>(kv + T::BYTES, &tmV, &kv_full[kvb], w.krow0, vh, vb);
-        ++c;
-        QueryTiles qt(w);
-        for (int j = 0; ok && j < w.n; ++j, qt.next()) {
-          const int h = w.hk * G + qt.head;
-          const int row = tile_row0(qt.t, kAttnTile, w.sq.ql);
-          for (int k = 0; k < 2; ++k, ++it) {
-            const int s = it % NS, use = it / NS;
-            if ((use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) || *abort_flag) {
-              ok = false;
-              break;
+  if (warp >= 16) {
+    regs_release<kBRegsProducer>();
+    if (warp == kBWarpTma) {
+      // --------------------------------------------------------------- TMA
+      if (elect_one()) {
+        bool ok = true;
+        int c = 0, it = 0;   // pieces and ring items so far
+        for (Rounds rd(total, (unsigned)A.dkv_ctas); ok && rd.more(); rd.next()) {
+          if (rd.index() >= total) continue;
+          const DkvItem w(A, rd.index());
+          if (w.n == 0) continue;
+          const int kb = (A.bcast & 2) ? 0 : w.b, kh = (A.bcast & 16) ? 0 : w.hk;
+          const int vb = (A.bcast & 4) ? 0 : w.b, vh = (A.bcast & 32) ? 0 : w.hk;
+          const int qb = (A.bcast & 1) ? 0 : w.b, gb = (A.bcast & 64) ? 0 : w.b;
+          const int kvb = c % KB, used = c / KB;
+          if (used > 0 && !(ok = mbar_wait(&kv_empty[kvb], (uint32_t)((used - 1) & 1)))) break;
+          uint8_t* kv = smem + L::K_OFF + kvb * 2 * T::BYTES;
+          mbar_arrive_expect_tx(&kv_full[kvb], 2 * T::BYTES);
+          load_tile<DP>(kv, &tmK, &kv_full[kvb], w.krow0, kh, kb);
+          load_tile<DP>(kv + T::BYTES, &tmV, &kv_full[kvb], w.krow0, vh, vb);
+          ++c;
+          QueryTiles qt(w);
+          for (int j = 0; ok && j < w.n; ++j, qt.next()) {
+            const int h = w.hk * G + qt.head;
+            const int row = tile_row0(qt.t, kAttnTile, w.sq.ql);
+            for (int k = 0; k < 2; ++k, ++it) {
+              const int s = it % NS, use = it / NS;
+              if ((use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) || *abort_flag) {
+                ok = false;
+                break;
+              }
+              uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
+              mbar_arrive_expect_tx(&full[s], T::BYTES);
+              if (k) load_tile<DP>(dst, &tmG, &full[s], row, (A.bcast & 128) ? 0 : h, gb);
+              else load_tile<DP>(dst, &tmQ, &full[s], row, (A.bcast & 8) ? 0 : h, qb);
             }
-            uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
-            mbar_arrive_expect_tx(&full[s], T::BYTES);
-            if (k) load_tile<DP>(dst, &tmG, &full[s], row, (A.bcast & 128) ? 0 : h, gb);
-            else load_tile<DP>(dst, &tmQ, &full[s], row, (A.bcast & 8) ? 0 : h, qb);
           }
         }
+        if (!ok) {
+          record_error(A.err, kErrAttnDkvTmaWait);
+          *abort_flag = 1;
+        }
+        // every load lands before the CTA can exit
+        for (int x = max(0, it - NS); x < it; ++x)
+          mbar_wait_sleep(&full[x % NS], (uint32_t)((x / NS) & 1));
+        for (int x = max(0, c - KB); x < c; ++x)
+          mbar_wait_sleep(&kv_full[x % KB], (uint32_t)((x / KB) & 1));
       }
-      if (!ok) {
-        record_error(A.err, kErrAttnDkvTmaWait);
-        *abort_flag = 1;
-      }
-      // every load lands before the CTA can exit
-      for (int x = max(0, it - NS); x < it; ++x)
-        mbar_wait_sleep(&full[x % NS], (uint32_t)((x / NS) & 1));
-      for (int x = max(0, c - KB); x < c; ++x)
-        mbar_wait_sleep(&kv_full[x % KB], (uint32_t)((x / KB) & 1));
-    }
-    __syncwarp();
-  } else if (warp == kBWarpMma) {
-    // --------------------------------------------------------------- MMA
-    if (elect_one()) {
-      constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
-      const uint64_t dK = T::k_major(smem_u32(smem + L::K_OFF));
-      const uint32_t ring = smem_u32(smem + L::RING_OFF);
-      const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
-      auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
-      auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
-      // S^T or dP^T: A = keys' tile, B = ring tile
-      auto issue_nt = [&](uint32_t d, uint64_t a, int it, uint64_t* bar) {
-        const uint64_t bd = rK + slot(it);
+      __syncwarp();
+    } else if (warp == kBWarpMma) {
+      // --------------------------------------------------------------- MMA
+      if (elect_one()) {
+        constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
+        const uint64_t dK = T::k_major(smem_u32(smem + L::K_OFF));
+        const uint32_t ring = smem_u32(smem + L::RING_OFF);
+        const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
+        auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
+        auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
+        // S^T or dP^T: A = keys' tile, B = ring tile
+        auto issue_nt = [&](uint32_t d, uint64_t a, int it, uint64_t* bar) {
+          const uint64_t bd = rK + slot(it);
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-          mma_ss(tmem + d, a + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
-        mma_commit(bar);
-      };
-      // dV or dK: A = P^T or dS^T in TMEM, B = ring tile, 128 queries deep
-      auto issue_nn = [&](uint32_t d, uint32_t a, int it, bool start) {
-        const uint64_t bd = rM + slot(it);
+          for (int kk = 0; kk < KS; ++kk)
+            mma_ss(tmem + d, a + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+          mma_commit(bar);
+        };
+        // dV or dK: A = P^T or dS^T in TMEM, B = ring tile, 128 queries deep
+        auto issue_nn = [&](uint32_t d, uint32_t a, int it, bool start) {
+          const uint64_t bd = rM + slot(it);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + d, tmem + a + a_step(kk), bd + kk * T::MN_STEP, idD,
-                 (!start || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[it % NS]);
-      };
-      auto kv = [&](int c) { return dK + ((uint32_t)((c % KB) * 2 * T::BYTES) >> 4); };
-      // S or dP of the tile at a cursor; K and V of its piece have landed
-      auto issue_S = [&](const Cursor& x) -> bool {
-        if (x.j == 0 && !mbar_wait(&kv_full[x.c % KB], (uint32_t)((x.c / KB) & 1))) return false;
-        if (!landed(2 * x.J)) return false;
-        tc_fence_after();
-        issue_nt(128 * (x.J % SB), kv(x.c), 2 * x.J, &s_full[x.J % SB]);
-        return true;
-      };
-      auto issue_dP = [&](const Cursor& x) -> bool {
-        if (!landed(2 * x.J + 1)) return false;
-        tc_fence_after();
-        issue_nt(TP, kv(x.c) + (T::BYTES >> 4), 2 * x.J + 1, dp_full);
-        if (x.last()) mma_commit(&kv_empty[x.c % KB]);   // S was issued before
-        return true;
-      };
-      // x: the tile whose dV and dK come next; xs, xp: the next S and dP
-      Cursor x, xs, xp;
-      Rounds rd(total);
-      bool ok = true;
-      auto next_S = [&]() {
-        if (xs.step()) xs.find(A, rd, ns);
-      };
-      auto next_dP = [&]() {
-        if (xp.step()) xp.follow(ns);
-      };
-      xs.find(A, rd, ns);
-      xp.follow(ns);
-      x.follow(ns);
-      // S runs SB tiles ahead, dP one; into the next piece only where its K
-      // and V have a buffer of their own
-      auto may = [&](const Cursor& y) { return y.on() && (KB == 2 || y.c == x.c); };
-      int c = 0;   // pieces complete
-      while (x.on()) {
-        if (x.j == 0 && (KB == 1 || x.J == 0)) {   // nothing of this piece is under way
-          for (int k = 0; ok && k < SB && may(xs); ++k) {
-            if ((ok = issue_S(xs))) next_S();
-            if (k == 0 && ok && (ok = issue_dP(xp))) next_dP();
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + d, tmem + a + a_step(kk), bd + kk * T::MN_STEP, idD,
+                   (!start || kk > 0) ? 1u : 0u);
+          mma_commit(&empty[it % NS]);
+        };
+        auto kv = [&](int c) { return dK + ((uint32_t)((c % KB) * 2 * T::BYTES) >> 4); };
+        // S or dP of the tile at a cursor; K and V of its piece have landed
+        auto issue_S = [&](const Cursor& x) -> bool {
+          if (x.j == 0 && !mbar_wait(&kv_full[x.c % KB], (uint32_t)((x.c / KB) & 1))) return false;
+          if (!landed(2 * x.J)) return false;
+          tc_fence_after();
+          issue_nt(128 * (x.J % SB), kv(x.c), 2 * x.J, &s_full[x.J % SB]);
+          return true;
+        };
+        auto issue_dP = [&](const Cursor& x) -> bool {
+          if (!landed(2 * x.J + 1)) return false;
+          tc_fence_after();
+          issue_nt(TP, kv(x.c) + (T::BYTES >> 4), 2 * x.J + 1, dp_full);
+          if (x.last()) mma_commit(&kv_empty[x.c % KB]);   // S was issued before
+          return true;
+        };
+        // x: the tile whose dV and dK come next; xs, xp: the next S and dP
+        Cursor x, xs, xp;
+        Rounds rd(total, (unsigned)A.dkv_ctas);
+        bool ok = true;
+        auto next_S = [&]() {
+          if (xs.step()) xs.find(A, rd, ns);
+        };
+        auto next_dP = [&]() {
+          if (xp.step()) xp.follow(ns);
+        };
+        xs.find(A, rd, ns);
+        xp.follow(ns);
+        x.follow(ns);
+        // S runs SB tiles ahead, dP one; into the next piece only where its K
+        // and V have a buffer of their own
+        auto may = [&](const Cursor& y) { return y.on() && (KB == 2 || y.c == x.c); };
+        int c = 0;   // pieces complete
+        while (x.on()) {
+          if (x.j == 0 && (KB == 1 || x.J == 0)) {   // nothing of this piece is under way
+            for (int k = 0; ok && k < SB && may(xs); ++k) {
+              if ((ok = issue_S(xs))) next_S();
+              if (k == 0 && ok && (ok = issue_dP(xp))) next_dP();
+            }
+            if (!ok) break;
           }
-          if (!ok) break;
+          const int J = x.J;
+          if (!(ok = mbar_wait(&p_ready[J % SB], (uint32_t)((J / SB) & 1)))) break;
+          if (x.j == 0 && c > 0 && !(ok = mbar_wait(acc_free, (uint32_t)((c - 1) & 1)))) break;
+          tc_fence_after();
+          issue_nn(TV, 128 * (J % SB), 2 * J + 1, x.j == 0);
+          if (may(xs)) {
+            if (!(ok = issue_S(xs))) break;
+            next_S();
+          }
+          if (!(ok = mbar_wait(ds_ready, (uint32_t)(J & 1)))) break;
+          tc_fence_after();
+          issue_nn(TK, TP, 2 * J, x.j == 0);
+          if (x.last()) {
+            mma_commit(done);
+            ++c;
+          }
+          if (may(xp)) {
+            if (!(ok = issue_dP(xp))) break;
+            next_dP();
+          }
+          if (*abort_flag) {
+            ok = false;
+            break;
+          }
+          if (x.step()) x.follow(ns);
         }
-        const int J = x.J;
-        if (!(ok = mbar_wait(&p_ready[J % SB], (uint32_t)((J / SB) & 1)))) break;
-        if (x.j == 0 && c > 0 && !(ok = mbar_wait(acc_free, (uint32_t)((c - 1) & 1)))) break;
-        tc_fence_after();
-        issue_nn(TV, 128 * (J % SB), 2 * J + 1, x.j == 0);
-        if (may(xs)) {
-          if (!(ok = issue_S(xs))) break;
-          next_S();
-        }
-        if (!(ok = mbar_wait(ds_ready, (uint32_t)(J & 1)))) break;
-        tc_fence_after();
-        issue_nn(TK, TP, 2 * J, x.j == 0);
-        if (x.last()) {
+        if (!ok) {
+          record_error(A.err, kErrAttnDkvMmaWait);
+          *abort_flag = 1;
           mma_commit(done);
           ++c;
         }
-        if (may(xp)) {
-          if (!(ok = issue_dP(xp))) break;
-          next_dP();
-        }
-        if (*abort_flag) {
-          ok = false;
-          break;
-        }
-        if (x.step()) x.follow(ns);
+        // every product is complete before the CTA can exit
+        if (c > 0) mbar_wait_sleep(done, (uint32_t)((c - 1) & 1));
       }
-      if (!ok) {
-        record_error(A.err, kErrAttnDkvMmaWait);
-        *abort_flag = 1;
-        mma_commit(done);
-        ++c;
-      }
-      // every product is complete before the CTA can exit
-      if (c > 0) mbar_wait_sleep(done, (uint32_t)((c - 1) & 1));
-    }
-    __syncwarp();
-  } else if (warp == kBWarpAux) {
-    // --------------------------- nl and delta of each tile's 128 columns
-    // Columns before the tile's own queries (a last tile moved back) get
-    // nl = -inf: weight 0.  With a piece's first tile goes the piece itself,
-    // one without a tile at the end; pieces without a tile are zeros, written
-    // here.
-    bool ok = true;
-    int J = 0, c = 0;
-    auto slot_free = [&]() -> bool {
-      const int use = J / NB;
-      return use == 0 || warp_all(mbar_wait_sleep(&nl_empty[J % NB], (uint32_t)((use - 1) & 1)));
-    };
-    for (Rounds rd(total); ok && rd.more(); rd.next()) {
-      if (rd.index() >= total) continue;
-      const DkvItem w(A, rd.index());
-      if (w.n == 0) {
-        const int rows = min(kAttnTile, A.Nk - w.k0);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int v = 0; v < 2; ++v) {
-          const Tok& to = v ? A.dv : A.dk;
-          __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + w.b * to.sb + w.hk * to.sh;
-          float* rec = A.dkv_part + ((((int64_t)w.bh * A.ktiles + w.kt) * A.dkv_splits + w.split) * 2 + v) *
-                                        kAttnTile * DP;
-          if (A.dkv_splits > 1) {
-            for (int x = lane; x < kAttnTile * DP / 4; x += 32) reinterpret_cast<uint4*>(rec)[x] = zero;
-          } else {
-            const int per_row = A.D / 8;
-            for (int x = lane; x < rows * per_row; x += 32) {
-              const int row = x / per_row;
-              *reinterpret_cast<uint4*>(out + (w.k0 + row) * to.sn + (x - row * per_row) * 8) = zero;
+      __syncwarp();
+    } else if (warp == kBWarpAux) {
+      // --------------------------- nl and delta of each tile's 128 columns
+      // Columns before the tile's own queries (a last tile moved back) get
+      // nl = -inf: weight 0.  With a piece's first tile goes the piece itself,
+      // one without a tile at the end; pieces without a tile are zeros, written
+      // here.
+      bool ok = true;
+      int J = 0, c = 0;
+      auto slot_free = [&]() -> bool {
+        const int use = J / NB;
+        return use == 0 || warp_all(mbar_wait_sleep(&nl_empty[J % NB], (uint32_t)((use - 1) & 1)));
+      };
+      for (Rounds rd(total, (unsigned)A.dkv_ctas); ok && rd.more(); rd.next()) {
+        if (rd.index() >= total) continue;
+        const DkvItem w(A, rd.index());
+        if (w.n == 0) {
+          const int rows = min(kAttnTile, A.Nk - w.k0);
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int v = 0; v < 2; ++v) {
+            const Tok& to = v ? A.dv : A.dk;
+            __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + w.b * to.sb + w.hk * to.sh;
+            float* rec = A.dkv_part + ((((int64_t)w.bh * A.ktiles + w.kt) * A.dkv_splits + w.split) * 2 + v) *
+                                          kAttnTile * DP;
+            if (A.dkv_splits > 1) {
+              for (int x = lane; x < kAttnTile * DP / 4; x += 32) reinterpret_cast<uint4*>(rec)[x] = zero;
+            } else {
+              const int per_row = A.D / 8;
+              for (int x = lane; x < rows * per_row; x += 32) {
+                const int row = x / per_row;
+                *reinterpret_cast<uint4*>(out + (w.k0 + row) * to.sn + (x - row * per_row) * 8) = zero;
+              }
             }
           }
+          continue;
         }
-        continue;
-      }
-      QueryTiles qt(w);
-      for (int j = 0; j < w.n; ++j, ++J, qt.next()) {
-        const int s = J % NB;
-        if (!(ok = slot_free())) break;
-        if (j == 0) {
-          if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = w;
-          ++c;
-        }
-        const int row0 = tile_row0(qt.t, kAttnTile, w.sq.ql);
-        const int64_t base = ((int64_t)w.b * A.Hq + w.hk * G + qt.head) * A.Nq;
-        float* dst = (float*)(smem + L::NL_OFF + s * 1024);
+        QueryTiles qt(w);
+        for (int j = 0; j < w.n; ++j, ++J, qt.next()) {
+          const int s = J % NB;
+          if (!(ok = slot_free())) break;
+          if (j == 0) {
+            if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = w;
+            ++c;
+          }
+          const int row0 = tile_row0(qt.t, kAttnTile, w.sq.ql);
+          const int64_t base = ((int64_t)w.b * A.Hq + w.hk * G + qt.head) * A.Nq;
+          float* dst = (float*)(smem + L::NL_OFF + s * 1024);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int col = 32 * k + lane, q = row0 + col;
-          const bool own = q >= qt.t * kAttnTile;
-          dst[col] = own ? A.nl[base + q] : -INFINITY;
-          dst[128 + col] = own ? A.delta[base + q] : 0.f;
+          for (int k = 0; k < 4; ++k) {
+            const int col = 32 * k + lane, q = row0 + col;
+            const bool own = q >= qt.t * kAttnTile;
+            dst[col] = own ? A.nl[base + q] : -INFINITY;
+            dst[128 + col] = own ? A.delta[base + q] : 0.f;
+          }
+          warp_arrive(&nl_full[s]);
         }
-        warp_arrive(&nl_full[s]);
+      }
+      if (ok && (ok = slot_free())) {
+        if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = DkvItem(A);
+        warp_arrive(&nl_full[J % NB]);
+      }
+      if (!ok) {
+        record_error(A.err, kErrAttnDkvRowWait);
+        *abort_flag = 1;
       }
     }
-    if (ok && (ok = slot_free())) {
-      if (lane == 0) *(DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64) = DkvItem(A);
-      warp_arrive(&nl_full[J % NB]);
-    }
-    if (!ok) {
-      record_error(A.err, kErrAttnDkvRowWait);
-      *abort_flag = 1;
-    }
-  } else if (warp < 16) {
+  } else {
+    regs_acquire<kBRegsSoftmax>();
     // ----------------------------------------------------- softmax warps
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;   // TMEM lane: key krow0 + r
@@ -539,15 +545,18 @@ __global__ void __launch_bounds__(kBThreads, 1)
     int J = 0;
     for (int c = 0;; ++c) {
       if (!(ok = warp_all(mbar_wait(&nl_full[J % NB], (uint32_t)((J / NB) & 1))))) break;
-      const DkvItem it = *(const DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64);
-      if (it.n == 0) break;
-      QueryTiles qt(it);
-      for (int j = 0; j < it.n; ++j, ++J, qt.next()) {
+      // the piece stays in its slot until this warp has stored its sums: the
+      // next two at most are published before that
+      const DkvItem* item = (const DkvItem*)(smem + L::ITEM_OFF + (c & 3) * 64);
+      const int n = item->n, krow0 = item->krow0, off = item->sq.off, ql = item->sq.ql;
+      if (n == 0) break;
+      QueryTiles qt(*item);
+      for (int j = 0; j < n; ++j, ++J, qt.next()) {
         const int s = J % NB;
         const uint32_t tS = tmem + lb + 128 * (J % SB) + kCols * w;
-        const int row0 = tile_row0(qt.t, kAttnTile, it.sq.ql);
+        const int row0 = tile_row0(qt.t, kAttnTile, ql);
         // columns below cl do not see this lane's key
-        const int cl = it.sq.causal ? it.krow0 + r - it.sq.off - row0 - kCols * w : -1;
+        const int cl = A.causal ? krow0 + r - off - row0 - kCols * w : -1;
         const float* nl = (const float*)(smem + L::NL_OFF + s * 1024) + kCols * w;
         ok &= mbar_wait(&nl_full[s], (uint32_t)((J / NB) & 1));
         float nv[kCols];   // read ahead of the wait for S
@@ -592,6 +601,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (!ok || !(ok = warp_all(mbar_wait(done, (uint32_t)(c & 1))))) break;
       __syncwarp();
       tc_fence_after();
+      const DkvItem it = *item;
       // warpgroups 0 and 1 store dK, 2 and 3 dV: this tile's own keys, then
       // zeros for the rows past the length
       const int key = it.krow0 + r, v = w >> 1;
@@ -629,7 +639,7 @@ template <int DP>
 struct DqLayout {
   using T = Tile<DP>;
   // ring of K and V tiles in the order K0 V0 K1 V1 ...
-  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 9 : 14;
+  static constexpr int SLOTS = DP == 128 ? 5 : DP == 64 ? 9 : 8;
   static constexpr int Q_OFF = 0;
   static constexpr int G_OFF = T::BYTES;
   static constexpr int RING_OFF = 2 * T::BYTES;
@@ -640,12 +650,9 @@ struct DqLayout {
 };
 
 template <int KS>
-__global__ void __launch_bounds__(kBThreads, 1)
-    attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-                   const __grid_constant__ AttnBwdArgs A) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                        const CUtensorMap& tmV, const CUtensorMap& tmG,
+                                        const AttnBwdArgs& A) {
   constexpr int DP = attn_dp(16 * KS);
   using L = DqLayout<DP>;
   using T = Tile<DP>;
@@ -666,11 +673,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- this CTA's work
-  unsigned u = blockIdx.x;
+  const unsigned idx = blockIdx.x - (unsigned)A.dkv_ctas;
+  unsigned u = idx;
   int split = 0;
   if (A.dq_splits > 1) {
-    u = blockIdx.x / (unsigned)A.dq_splits;
-    split = (int)(blockIdx.x - u * A.dq_splits);
+    u = idx / (unsigned)A.dq_splits;
+    split = (int)(idx - u * A.dq_splits);
   }
   // causal: longest rows first
   const unsigned inner = A.causal ? (unsigned)(A.B * A.Hq) : (unsigned)A.qtiles;
@@ -704,105 +712,109 @@ __global__ void __launch_bounds__(kBThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kBWarpTma) {
-    // --------------------------------------------------------------- TMA
-    if (n > 0 && elect_one()) {
-      const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
-      const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
-      mbar_arrive_expect_tx(q_full, 2 * T::BYTES);
-      load_tile<DP>(smem + L::Q_OFF, &tmQ, q_full, q0, (A.bcast & 8) ? 0 : h, (A.bcast & 1) ? 0 : b);
-      load_tile<DP>(smem + L::G_OFF, &tmG, q_full, q0, (A.bcast & 128) ? 0 : h,
-                    (A.bcast & 64) ? 0 : b);
-      int last = -1;
-      for (int it = 0; it < 2 * n; ++it) {
-        const int s = it % NS, use = it / NS;
-        if (use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) {
-          record_error(A.err, kErrAttnDqTmaWait);
+  if (warp >= 16) {
+    regs_release<kBRegsProducer>();
+    if (warp == kBWarpTma) {
+      // --------------------------------------------------------------- TMA
+      if (n > 0 && elect_one()) {
+        const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
+        const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
+        mbar_arrive_expect_tx(q_full, 2 * T::BYTES);
+        load_tile<DP>(smem + L::Q_OFF, &tmQ, q_full, q0, (A.bcast & 8) ? 0 : h, (A.bcast & 1) ? 0 : b);
+        load_tile<DP>(smem + L::G_OFF, &tmG, q_full, q0, (A.bcast & 128) ? 0 : h,
+                      (A.bcast & 64) ? 0 : b);
+        int last = -1;
+        for (int it = 0; it < 2 * n; ++it) {
+          const int s = it % NS, use = it / NS;
+          if (use > 0 && !mbar_wait(&empty[s], (uint32_t)((use - 1) & 1))) {
+            record_error(A.err, kErrAttnDqTmaWait);
+            *abort_flag = 1;
+            break;
+          }
+          if (*abort_flag) break;
+          const int row = tile_row0(lo + (it >> 1), kAttnTile, sq.kl);
+          uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
+          mbar_arrive_expect_tx(&full[s], T::BYTES);
+          if (it & 1) load_tile<DP>(dst, &tmV, &full[s], row, vh, vb);
+          else load_tile<DP>(dst, &tmK, &full[s], row, kh, kb);
+          last = it;
+        }
+        for (int it = max(0, last - NS + 1); it <= last; ++it)
+          mbar_wait_sleep(&full[it % NS], (uint32_t)((it / NS) & 1));
+        mbar_wait_sleep(q_full, 0);
+      }
+      __syncwarp();
+    } else if (warp == kBWarpMma) {
+      // --------------------------------------------------------------- MMA
+      if (n > 0 && elect_one()) {
+        constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
+        const uint64_t dQ = T::k_major(smem_u32(smem + L::Q_OFF));
+        const uint64_t dG = T::k_major(smem_u32(smem + L::G_OFF));
+        const uint32_t ring = smem_u32(smem + L::RING_OFF);
+        const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
+        auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
+        auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
+        auto issue_S = [&](int j) {
+          const uint64_t bd = rK + slot(2 * j);
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk)
+            mma_ss(tmem + 128 * (j & 1), dQ + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+          mma_commit(&s_full[j & 1]);
+        };
+        auto issue_dP = [&](int j) {
+          const uint64_t bd = rK + slot(2 * j + 1);
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk)
+            mma_ss(tmem + TP, dG + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
+          mma_commit(dp_full);
+          mma_commit(&empty[(2 * j + 1) % NS]);
+        };
+        auto issue_dQ = [&](int j) {
+          const uint64_t bd = rM + slot(2 * j);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + TQ, tmem + TP + a_step(kk), bd + kk * T::MN_STEP, idD,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&empty[(2 * j) % NS]);
+        };
+        bool ok = mbar_wait(q_full, 0) && landed(0) && landed(1);
+        if (ok) {
+          tc_fence_after();
+          issue_S(0);
+          issue_dP(0);
+        }
+        if (ok && n > 1 && (ok = landed(2))) {
+          tc_fence_after();
+          issue_S(1);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
+          tc_fence_after();
+          issue_dQ(j);
+          if (j + 1 < n) {
+            if (!(ok = landed(2 * j + 3))) break;
+            tc_fence_after();
+            issue_dP(j + 1);
+          }
+          if (j + 2 < n) {
+            if (!(ok = landed(2 * j + 4))) break;
+            tc_fence_after();
+            issue_S(j + 2);
+          }
+          if (*abort_flag) ok = false;
+        }
+        if (!ok) {
+          record_error(A.err, kErrAttnDqMmaWait);
           *abort_flag = 1;
-          break;
         }
-        if (*abort_flag) break;
-        const int row = tile_row0(lo + (it >> 1), kAttnTile, sq.kl);
-        uint8_t* dst = smem + L::RING_OFF + s * T::BYTES;
-        mbar_arrive_expect_tx(&full[s], T::BYTES);
-        if (it & 1) load_tile<DP>(dst, &tmV, &full[s], row, vh, vb);
-        else load_tile<DP>(dst, &tmK, &full[s], row, kh, kb);
-        last = it;
+        mma_commit(done);
+        mbar_wait_sleep(done, 0);
       }
-      for (int it = max(0, last - NS + 1); it <= last; ++it)
-        mbar_wait_sleep(&full[it % NS], (uint32_t)((it / NS) & 1));
-      mbar_wait_sleep(q_full, 0);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == kBWarpMma) {
-    // --------------------------------------------------------------- MMA
-    if (n > 0 && elect_one()) {
-      constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
-      constexpr uint32_t idD = idesc_bf16_f32(128, 16 * KS, 0, 1);
-      const uint64_t dQ = T::k_major(smem_u32(smem + L::Q_OFF));
-      const uint64_t dG = T::k_major(smem_u32(smem + L::G_OFF));
-      const uint32_t ring = smem_u32(smem + L::RING_OFF);
-      const uint64_t rK = T::k_major(ring), rM = T::mn_major(ring);
-      auto slot = [&](int it) { return (uint32_t)((it % NS) * T::BYTES) >> 4; };
-      auto landed = [&](int it) { return mbar_wait(&full[it % NS], (uint32_t)((it / NS) & 1)); };
-      auto issue_S = [&](int j) {
-        const uint64_t bd = rK + slot(2 * j);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-          mma_ss(tmem + 128 * (j & 1), dQ + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
-        mma_commit(&s_full[j & 1]);
-      };
-      auto issue_dP = [&](int j) {
-        const uint64_t bd = rK + slot(2 * j + 1);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-          mma_ss(tmem + TP, dG + T::kstep(kk), bd + T::kstep(kk), idS, kk > 0);
-        mma_commit(dp_full);
-        mma_commit(&empty[(2 * j + 1) % NS]);
-      };
-      auto issue_dQ = [&](int j) {
-        const uint64_t bd = rM + slot(2 * j);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + TQ, tmem + TP + a_step(kk), bd + kk * T::MN_STEP, idD,
-                 (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[(2 * j) % NS]);
-      };
-      bool ok = mbar_wait(q_full, 0) && landed(0) && landed(1);
-      if (ok) {
-        tc_fence_after();
-        issue_S(0);
-        issue_dP(0);
-      }
-      if (ok && n > 1 && (ok = landed(2))) {
-        tc_fence_after();
-        issue_S(1);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = mbar_wait(ds_ready, (uint32_t)(j & 1)))) break;
-        tc_fence_after();
-        issue_dQ(j);
-        if (j + 1 < n) {
-          if (!(ok = landed(2 * j + 3))) break;
-          tc_fence_after();
-          issue_dP(j + 1);
-        }
-        if (j + 2 < n) {
-          if (!(ok = landed(2 * j + 4))) break;
-          tc_fence_after();
-          issue_S(j + 2);
-        }
-        if (*abort_flag) ok = false;
-      }
-      if (!ok) {
-        record_error(A.err, kErrAttnDqMmaWait);
-        *abort_flag = 1;
-      }
-      mma_commit(done);
-      mbar_wait_sleep(done, 0);
-    }
-    __syncwarp();
-  } else if (warp < 16) {
+  } else {
+    regs_acquire<kBRegsSoftmax>();
     // ----------------------------------------------------- softmax warps
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
@@ -866,8 +878,22 @@ __global__ void __launch_bounds__(kBThreads, 1)
   if (warp == kBWarpMma) tmem_dealloc(tmem, 512);
 }
 
+// Both in one launch, so that dQ's CTAs fill the SMs that the last of dK's and
+// dV's leave idle (2 x 8 heads of 6000, D 64, 5.1 waves each: 607 us as two
+// launches, 567 as one; 16/4 heads of 4096, D 128: 385 and 364).
 template <int KS>
-cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
+__global__ void __launch_bounds__(kBThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ AttnBwdArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x < (unsigned)A.dkv_ctas) attn_dkv<KS>(tmQ, tmK, tmV, tmG, A);
+  else attn_dq<KS>(tmQ, tmK, tmV, tmG, A);
+}
+
+template <int KS>
+cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, AttnBwdArgs a, cudaStream_t st) {
   constexpr int DP = attn_dp(16 * KS);
   CUtensorMap mq, mk, mv, mg;
   cudaError_t e;
@@ -875,22 +901,20 @@ cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
   if ((e = attn_map(&mk, a.K, d.k, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
   if ((e = attn_map(&mv, a.V, d.v, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
   if ((e = attn_map(&mg, a.dY, d.dy, d.B, d.Hq, d.Nq, d.D, DP, 128, 1)) != cudaSuccess) return e;
-  auto go = [&](auto kernel, int64_t grid, int bytes) {
-    const int smem = bytes > kMinSmemBytes ? bytes : kMinSmemBytes;
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (r != cudaSuccess) return r;
-    r = launch_pdl(kernel, dim3((unsigned)grid), kBThreads, smem, st, mq, mk, mv, mg, a);
-    return r != cudaSuccess ? r : cudaPeekAtLastError();
-  };
-  // CTAs stay for several pieces where a piece is short (256 latents over
-  // 65,536 tokens, D 64: 2 query tiles a piece)
-  const int64_t pieces = p.dkv_units * p.dkv_splits;
+  // CTAs stay for several pieces of dK and dV where a piece is short (256
+  // latents over 65,536 tokens, D 64: 2 query tiles a piece)
+  const int64_t pieces = a.dK ? p.dkv_units * p.dkv_splits : 0;
   const bool stay = DkvLayout<DP>::KB == 2 && d.G() * p.qtiles <= 8 * p.dkv_splits;
-  if (a.dK && (e = go(attn_dkv_kernel<KS>, stay ? imin64(pieces, sm_count()) : pieces,
-                      DkvLayout<DP>::BYTES)) != cudaSuccess)
+  a.dkv_ctas = (int)(stay ? imin64(pieces, sm_count()) : pieces);
+  const int64_t grid = a.dkv_ctas + (a.dQ ? p.dq_units * p.dq_splits : 0);
+  constexpr int kBytes =
+      DkvLayout<DP>::BYTES > DqLayout<DP>::BYTES ? DkvLayout<DP>::BYTES : DqLayout<DP>::BYTES;
+  constexpr int kSmem = kBytes > kMinSmemBytes ? kBytes : kMinSmemBytes;
+  if ((e = cudaFuncSetAttribute(attn_bwd_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem)) != cudaSuccess)
     return e;
-  if (a.dQ) e = go(attn_dq_kernel<KS>, p.dq_units * p.dq_splits, DqLayout<DP>::BYTES);
-  return e;
+  e = launch_pdl(attn_bwd_kernel<KS>, dim3((unsigned)grid), kBThreads, kSmem, st, mq, mk, mv, mg, a);
+  return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
 }  // namespace
