@@ -364,18 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < nw; ++j) {
       const int t = lo + (QT == 2 ? j : 2 * j + w);
-      if (!warp_all(mbar_wait(&s_full[w], (uint32_t)(j & 1)))) {
-        ok = false;
-        break;
-      }
+      ok &= mbar_wait(&s_full[w], (uint32_t)(j & 1));
       if (!warp_live) {   // no row of this warp is stored
         warp_arrive(&early[w]);
         // not ahead of the other warps' P of the tile before
-        if (APART && j > 0 && !warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
-          ok = false;
-          break;
-        }
+        if (APART && j > 0) ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
         warp_arrive(&p_ready[w]);
+        if (!(ok = warp_all(ok))) break;
         continue;
       }
       __syncwarp();
@@ -401,10 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       max_fold64(a[1], m4);
       const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
       if (APART && j > 0) {   // the last product has read P (and O may be rescaled)
-        if (!warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
-          ok = false;
-          break;
-        }
+        ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
         __syncwarp();
         tc_fence_after();
       }
@@ -416,10 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mr = nm;
         if (j > 0) {
           if (!APART) {
-            if (!warp_all(mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1)))) {
-              ok = false;
-              break;
-            }
+            ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
             __syncwarp();
             tc_fence_after();
           }
@@ -457,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(&p_ready[w]);
       l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      if (!(ok = warp_all(ok))) break;   // a wait ran out: one vote for all
     }
     if (ok && nw > 0 && !warp_all(mbar_wait(&pv_done[w], (uint32_t)((nw - 1) & 1)))) ok = false;
     if (!ok) {
