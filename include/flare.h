@@ -570,6 +570,11 @@ FLARE_API flare_status_t flare_eval_exp2(const float* x, float* y, int64_t n, in
  * scale finite and > 0.  K and V of a key that the mask hides from a query,
  * but that lies within k_lens, have to be finite.  Results do not depend on
  * timing (no atomics).  Enqueued on `stream`.
+ * Not finite: a query that sees a logit of NaN or +inf has Y = NaN and
+ * lse = NaN (and NaN in its dQ, and in dK and dV of its batch and key head);
+ * logits of -inf have no weight, and a query with no other logit counts as one
+ * that sees no key.  Finite logits have to stay below 2^30 in magnitude (in
+ * float32 they are off by 2^-23 of it: weights mean little long before that).
  */
 FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void* Y,
                                         const flare_strides_t* strides, const int32_t* q_lens,

@@ -140,14 +140,21 @@ __device__ __forceinline__ void mask_cols(uint32_t (&a)[N], int col0, int lo, in
     if (col0 + t < lo || col0 + t > hi) a[t] = 0xff800000u;
 }
 
-// Max of 64 values folded into four independent accumulators.
+// Three-input maximum that is NaN when one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Max of 64 values folded into four independent accumulators (NaN: one was).
 __device__ __forceinline__ void max_fold64(const uint32_t (&a)[64], float (&m)[4]) {
 #pragma unroll
   for (int t = 0; t < 64; t += 8) {
-    m[0] = max3(m[0], __uint_as_float(a[t + 0]), __uint_as_float(a[t + 1]));
-    m[1] = max3(m[1], __uint_as_float(a[t + 2]), __uint_as_float(a[t + 3]));
-    m[2] = max3(m[2], __uint_as_float(a[t + 4]), __uint_as_float(a[t + 5]));
-    m[3] = max3(m[3], __uint_as_float(a[t + 6]), __uint_as_float(a[t + 7]));
+    m[0] = max3_nan(m[0], __uint_as_float(a[t + 0]), __uint_as_float(a[t + 1]));
+    m[1] = max3_nan(m[1], __uint_as_float(a[t + 2]), __uint_as_float(a[t + 3]));
+    m[2] = max3_nan(m[2], __uint_as_float(a[t + 4]), __uint_as_float(a[t + 5]));
+    m[3] = max3_nan(m[3], __uint_as_float(a[t + 6]), __uint_as_float(a[t + 7]));
   }
 }
 

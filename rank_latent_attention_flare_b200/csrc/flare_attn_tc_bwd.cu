@@ -565,16 +565,17 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& tmQ, const CUtensorM
           const float4 v = *reinterpret_cast<const float4*>(nl + x);
           nv[x] = v.x, nv[x + 1] = v.y, nv[x + 2] = v.z, nv[x + 3] = v.w;
         }
-        const bool gone = nl[lane] == -INFINITY;
+        const bool odd = !(fabsf(nl[lane]) < INFINITY);
         ok &= mbar_wait(&s_full[J % SB], (uint32_t)((J / SB) & 1));
         __syncwarp();
         tc_fence_after();
         uint32_t p[kCols];
         tmem_ld32(tS, p);
         tmem_wait_ld_dep(p);
-        // a tile with masked columns or rows without weight keeps to the MUFU,
-        // whose exponential of -inf is 0
-        if (warp_any(cl > 0 || gone)) {
+        // a tile with masked columns, or queries without weight or with a NaN
+        // among their logits (and so in nl), keeps to the MUFU, whose exponential
+        // of -inf is 0 and of NaN is NaN
+        if (warp_any(cl > 0 || odd)) {
           mask_cols(p, 0, cl, kCols - 1);
           exp_cols<true, 0>(p, A.c, 0.f, nv);
         } else {
@@ -825,7 +826,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
     const int64_t row = bh * A.Nq + i;
     const float nl = live && i < sq.ql ? A.nl[row] : -INFINITY;
     const float delta = live && i < sq.ql ? A.delta[row] : 0.f;
-    const bool gone = nl == -INFINITY;
+    const bool gone = nl == -INFINITY, odd = !(fabsf(nl) < INFINITY);   // as for dK and dV
     const float none[1] = {0.f};
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -839,7 +840,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
       uint32_t p[kCols];
       tmem_ld32(tmem + lb + 128 * (j & 1) + kCols * w, p);
       tmem_wait_ld_dep(p);
-      if (warp_any(cl > 0 || ch < kCols - 1 || gone)) {
+      if (warp_any(cl > 0 || ch < kCols - 1 || odd)) {
         mask_cols(p, 0, cl, ch);
         exp_cols<false, 0>(p, A.c, nl, none);
       } else {

@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool warp_live = warp_any(live && i < sq.ql);
     const int nw = QT == 2 ? (w ? n1 : n0) : (n - w + 1) / 2;   // tiles of this warpgroup
     float mr = -INFINITY, l = 0.f;
+    float top = -INFINITY;   // the largest logit so far; NaN once there was one
     bool ok = true;
     for (int j = 0; j < nw; ++j) {
       const int t = lo + (QT == 2 ? j : 2 * j + w);
@@ -394,13 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       max_fold64(a[0], m4);
       max_fold64(a[1], m4);
-      const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+      const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+      top = max3_nan(top, mx, mx);
       if (APART && j > 0) {   // the last product has read P (and O may be rescaled)
         ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
         __syncwarp();
         tc_fence_after();
       }
-      const bool move = (mx - mr) * A.c > kRescaleTau;
+      const bool move = (mx - mr) * A.c > kRescaleTau;   // not for NaN
       if (warp_any(move)) {
         const float nm = move ? mx : mr;
         const float f = move ? ex2((mr - nm) * A.c) : 1.f;
@@ -454,6 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       *abort_flag = 1;
       l = 0.f;
     }
+    // The FMA pipe's exponentials clamp what they get to finite weights.  A NaN or
+    // +inf among the logits makes the row NaN all the same, by its sum; a row with
+    // nothing above -inf has no weight.
+    if (!(top < INFINITY)) l = __uint_as_float(0x7fffffffu);
+    else if (top == -INFINITY) l = 0.f;
     __syncwarp();
     tc_fence_after();
     float m2 = mr == -INFINITY ? -INFINITY : mr * A.c;   // reference, log2 units
