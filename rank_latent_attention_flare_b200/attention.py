@@ -387,5 +387,9 @@ def attn(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
 def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float = 1e-6,
                  interleaved: bool = False):
     """Per-head norms and position rotation with autograd (arguments as
-    qk_norm_rope_fwd); returns (qo, ko)."""
+    qk_norm_rope_fwd); returns (qo, ko).  Gradients go to q, k, wq and wk: cos
+    and sin that need one are refused."""
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} gets no gradient; pass {name}.detach()")
     return QkNormRopeFunction.apply(q, k, wq, wk, cos, sin, eps, interleaved)
