@@ -311,6 +311,12 @@ def qk_norm_rope_bwd(q, k, wq, wk, cos, sin, dqo, dko, *, eps: float = 1e-6,
 
 # -------------------------------------------------------------------- autograd
 
+def _no_gradient(name: str, t):
+    """Refuses an argument that the backward gives no gradient to."""
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} gets no gradient; pass {name}.detach()")
+
+
 def _grad_view(t: torch.Tensor) -> torch.Tensor:
     """An upstream gradient the library reads in place, else a contiguous copy."""
     if t.is_contiguous() and t.data_ptr() % 16 == 0:
@@ -380,7 +386,9 @@ class QkNormRopeFunction(torch.autograd.Function):
 def attn(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
          q_lens: Optional[torch.Tensor] = None,
          k_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Softmax attention with autograd (arguments as attn_fwd)."""
+    """Softmax attention with autograd (arguments as attn_fwd).  Gradients go
+    to q, k and v: a scale that needs one is refused."""
+    _no_gradient("scale", scale)
     return AttnFunction.apply(q, k, v, scale, causal, q_lens, k_lens)
 
 
@@ -389,7 +397,6 @@ def qk_norm_rope(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float = 1e-
     """Per-head norms and position rotation with autograd (arguments as
     qk_norm_rope_fwd); returns (qo, ko).  Gradients go to q, k, wq and wk: cos
     and sin that need one are refused."""
-    for name, t in (("cos", cos), ("sin", sin)):
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} gets no gradient; pass {name}.detach()")
+    _no_gradient("cos", cos)
+    _no_gradient("sin", sin)
     return QkNormRopeFunction.apply(q, k, wq, wk, cos, sin, eps, interleaved)

@@ -30,3 +30,8 @@ def test_angles_without_a_graph():
     with torch.no_grad():
         got = fl.qk_norm_rope(q, k, None, None, cos, sin)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_scale_that_needs_a_gradient_is_refused():
+    with pytest.raises(ValueError, match="no gradient"):
+        fl.attn(*heads(), torch.tensor(0.5, requires_grad=True))
