@@ -79,6 +79,17 @@ def _shape(name: str, t, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
+def _output(name: str, t):
+    """A caller's output: its history in autograd would be the old one's."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} needs a gradient, and this call records none")
+
+
+# The library writes through raw pointers: autograd is told, so that a backward
+# that saved an overwritten tensor reports it.
+_written = torch.autograd.graph.increment_version
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -140,7 +151,7 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
     q [B,Hq,Nq,D]; k, v [B,Hk,Nk,D] with Hq a multiple of Hk (the query heads
     of a key head are neighbours); D a multiple of 8 up to 128.  All may be
     any views with D contiguous, k, v and q also expanded over batch or heads;
-    y takes q's layout.  ``q_lens``, ``k_lens`` (int32 [B] on the device):
+    y takes q's layout, or goes to ``out``.  ``q_lens``, ``k_lens`` (int32 [B] on the device):
     valid queries and keys; rows past them are never used and y is 0 there.
     ``causal``: query i sees keys j <= i + (keys - queries), counted with the
     lengths.  A query that sees no key gives 0."""
@@ -158,6 +169,7 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
             y = out
             _same("attention", q, y)
             _shape("out", y, q.shape)
+            _output("out", y)
         lse = low = None
         if save or save_low:
             lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
@@ -174,6 +186,8 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
             _p(low), ws.data_ptr(), ws.numel(), _raw_stream(index))
     if st:
         _lib.check(st, "flare_attn_fwd")
+    if out is not None:
+        _written(out)
     if save_low:
         return y, lse, low
     return (y, lse) if save else y
@@ -275,12 +289,16 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float =
             _same("query and key", q, qo, ko)
             _shape("out[0]", qo, q.shape)
             _shape("out[1]", ko, k.shape)
+            _output("out[0]", qo)
+            _output("out[1]", ko)
         st = _lib.load().flare_qk_norm_rope_fwd(
             q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(cos), _p(sin), sb, qo.data_ptr(),
             ko.data_ptr(), _strides(q, k, qo, ko), B, Hq, Hk, N, D, R, 1 if interleaved else 0,
             code, eps, _raw_stream(index))
     if st:
         _lib.check(st, "flare_qk_norm_rope_fwd")
+    if out is not None:
+        _written((qo, ko))
     return qo, ko
 
 

@@ -35,3 +35,38 @@ def test_angles_without_a_graph():
 def test_a_scale_that_needs_a_gradient_is_refused():
     with pytest.raises(ValueError, match="no gradient"):
         fl.attn(*heads(), torch.tensor(0.5, requires_grad=True))
+
+
+@pytest.mark.gpu
+def test_outputs_written_in_place_are_counted():
+    """A tensor that autograd saved and a call then overwrites: the backward
+    reports it."""
+    q, k, v = heads("cuda")
+    w = torch.ones(32, device="cuda", requires_grad=True)
+    for write in (lambda: fl.qk_norm_rope_fwd(q, k, out=(q, k)),
+                  lambda: fl.attn_fwd(q, k, v, out=q)):
+        loss = (w * q).sum()   # saves q
+        was = q._version
+        write()
+        assert q._version > was
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    assert k._version > 0
+
+
+@pytest.mark.gpu
+def test_outputs_of_a_graph_are_refused():
+    """An output that autograd holds a history of would keep the old one."""
+    q, k, v = heads("cuda")
+    x = (2.0 * q).requires_grad_()
+    for call in (lambda o: fl.attn_fwd(q, k, v, out=o),
+                 lambda o: fl.qk_norm_rope_fwd(q, k, out=(o, torch.empty_like(k))),
+                 lambda o: fl.qk_norm_rope_fwd(q, k, out=(torch.empty_like(k), o))):
+        with pytest.raises(ValueError, match="gradient"):
+            call(x)
+    with torch.no_grad():
+        assert fl.attn_fwd(q, k, v, out=x) is x
+    with torch.inference_mode():
+        y = torch.empty_like(q)
+        fl.attn_fwd(q, k, v, out=y)
+    assert torch.equal(x.detach(), y)
