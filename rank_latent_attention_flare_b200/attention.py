@@ -342,7 +342,8 @@ def _grad_view(t: torch.Tensor) -> torch.Tensor:
     esz = t.element_size()
     ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
         n == 1 or (s > 0 and (s * esz) % 16 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
-    return t if ok else t.contiguous()
+    # (contiguous() keeps a contiguous tensor, also where it is misaligned)
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 def _once(backward):

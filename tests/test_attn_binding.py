@@ -70,3 +70,31 @@ def test_outputs_of_a_graph_are_refused():
         y = torch.empty_like(q)
         fl.attn_fwd(q, k, v, out=y)
     assert torch.equal(x.detach(), y)
+
+
+def test_a_misaligned_gradient_is_copied():
+    """A gradient that begins inside a 16-byte group, contiguous or not."""
+    from rank_latent_attention_flare_b200.attention import _grad_view
+    buf = torch.arange(2 * 3 * 8 * 16 + 8, dtype=torch.bfloat16)
+    assert buf.data_ptr() % 16 == 0
+    for off in range(8):
+        t = buf[off:off + 2 * 3 * 8 * 16].view(2, 3, 8, 16)
+        for x in (t, t.transpose(1, 2)):
+            got = _grad_view(x)
+            assert got.data_ptr() % 16 == 0 and torch.equal(got, x)
+            assert (got.data_ptr() == x.data_ptr()) == (off == 0)
+
+
+@pytest.mark.gpu
+def test_a_misaligned_gradient_through_autograd():
+    q, k, v = (t.requires_grad_() for t in heads("cuda"))
+    flat = torch.randn(q.numel() + 1, device="cuda")
+    dy = flat[1:].view(q.shape)
+    y = fl.attn(q, k, v)
+    got = torch.autograd.grad(y, (q, k, v), dy, retain_graph=True)
+    want = torch.autograd.grad(y, (q, k, v), dy.clone())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    out = fl.qk_norm_rope(q, k)
+    got = torch.autograd.grad(out, (q, k), (dy, dy), retain_graph=True)
+    want = torch.autograd.grad(out, (q, k), (dy.clone(), dy.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
