@@ -408,6 +408,8 @@ def attn(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
     """Softmax attention with autograd (arguments as attn_fwd).  Gradients go
     to q, k and v: a scale that needs one is refused."""
     _no_gradient("scale", scale)
+    if not torch.is_grad_enabled():   # a Function would not know, and save for a backward
+        return attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens)
     return AttnFunction.apply(q, k, v, scale, causal, q_lens, k_lens)
 
 

@@ -98,3 +98,22 @@ def test_a_misaligned_gradient_through_autograd():
     got = torch.autograd.grad(out, (q, k), (dy, dy), retain_graph=True)
     want = torch.autograd.grad(out, (q, k), (dy.clone(), dy.clone()))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_without_a_graph_nothing_is_saved(monkeypatch):
+    """Parameters need gradients, the call is made under no_grad: y alone."""
+    import importlib
+    att = importlib.import_module("rank_latent_attention_flare_b200.attention")
+    asked = []
+
+    def fake(q, k, v, scale=None, **kw):
+        saving = kw.get("save") or kw.get("save_low")
+        asked.append(bool(saving))
+        return (q.clone(), q[..., 0].clone(), None) if saving else q.clone()
+    monkeypatch.setattr(att, "attn_fwd", fake)
+    q, k, v = (t.requires_grad_() for t in heads())
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            assert not fl.attn(q, k, v).requires_grad
+    assert fl.attn(q, k, v).requires_grad
+    assert asked == [False, False, True]
