@@ -610,6 +610,17 @@ FLARE_API size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, 
                                            int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dtype);
 
 /*
+ * How a call of these sizes is cut on the current device (queries not broadcast
+ * over the heads), for tests and tuning; the answer changes with the cost
+ * estimates behind it.  plan[0..2], backward = 0: query tiles a CTA takes, heads
+ * whose queries share a tile, parts of the keys; 1: parts of a piece of dK and
+ * dV, parts of one of dQ, whether a CTA stays for several pieces of dK and dV.
+ */
+FLARE_API flare_status_t flare_attn_plan(int backward, int64_t B, int64_t Hq, int64_t Hk,
+                                         int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dtype,
+                                         int causal, int64_t* plan);
+
+/*
  * Norm of every query and key head and rotation by position, in one pass:
  * per token and head, with weights w and the token's angles for the first R
  * of the D elements,

@@ -8,7 +8,7 @@ tensor-core kernels and CUDA-core kernels) behind the C ABI declared in
 from ._lib import (FLARE_BF16, FLARE_F32, FLARE_OP_BWD, FLARE_OP_FWD, FLARE_OP_PP_BWD,
                    FLARE_OP_PP_FWD,
                    NOALLOC_SCRATCH_BYTES, FlareError, LIB_PATH, SIGNATURES, load)
-from .attention import (AttnFunction, QkNormRopeFunction, attn, attn_bwd, attn_fwd,
+from .attention import (AttnFunction, QkNormRopeFunction, attn, attn_bwd, attn_fwd, attn_plan,
                         attn_workspace_size, qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_fwd)
 from .autograd import FlareFunction, FlarePPFunction, flare, flare_pp
 from .flare import (alloc_workspace, bwd_path, default_scale, device_status, encode_records,
@@ -31,7 +31,8 @@ __all__ = [
     "FlareFunction", "FlarePPFunction", "flare", "flare_pp",
     "encode_records", "flare_bwd_shard_dz", "flare_bwd_shard_finish", "flare_combine_shards",
     "records_layout", "parallel", "flare_pp_bwd_shard_tail", "noalloc_device_status",
-    "AttnFunction", "QkNormRopeFunction", "attn", "attn_bwd", "attn_fwd", "attn_workspace_size",
+    "AttnFunction", "QkNormRopeFunction", "attn", "attn_bwd", "attn_fwd", "attn_plan",
+    "attn_workspace_size",
     "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_fwd",
     "probe_unit_rates", "probe_mma_rates", "eval_exp2", "selftest_wait_timeout", "exp_split",
 ]

@@ -115,6 +115,7 @@ SIGNATURES = {
     "flare_attn_bwd": (_i32, [_vp] * 10 + [_vp] + [_vp] * 2 + [_i64] * 6 +
                        [_i32, _f32, _i32, _vp, _sz, _vp]),
     "flare_attn_workspace_size": (_sz, [_i32] + [_i64] * 6 + [_i32]),
+    "flare_attn_plan": (_i32, [_i32] + [_i64] * 6 + [_i32, _i32, _i64p]),
     "flare_qk_norm_rope_fwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 2 + [_vp] + [_i64] * 6 +
                                [_i32, _i32, _f32, _vp]),
     "flare_qk_norm_rope_bwd": (_i32, [_vp] * 6 + [_i64] + [_vp] * 6 + [_vp] + [_i64] * 6 +

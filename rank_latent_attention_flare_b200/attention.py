@@ -127,6 +127,18 @@ def attn_workspace_size(backward: bool, B: int, Hq: int, Hk: int, Nq: int, Nk: i
                                                      code))
 
 
+def attn_plan(backward: bool, B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int,
+              dtype: torch.dtype, causal: bool = False):
+    """How attn_fwd or attn_bwd cuts a call of these sizes on the current device
+    (flare_attn_plan): (query tiles a CTA, heads a tile, parts of the keys), or
+    (parts of dK and dV, parts of dQ, CTAs stay for several pieces)."""
+    code = _lib.FLARE_F32 if dtype == torch.float32 else _lib.FLARE_BF16
+    out = (ctypes.c_int64 * 3)()
+    _lib.check(_lib.load().flare_attn_plan(int(bool(backward)), B, Hq, Hk, Nq, Nk, D, code,
+                                           int(bool(causal)), out), "flare_attn_plan")
+    return tuple(out)
+
+
 def _attn_dims(q, k, v, *more):
     """The device's index and the sizes."""
     index = _same("attention", q, k, v, *more)

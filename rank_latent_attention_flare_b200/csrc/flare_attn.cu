@@ -147,6 +147,9 @@ AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
         if (c < best - 1e-9) best = c, at = (int)s;
       }
     }
+    // where a piece is short (256 latents over 65,536 tokens, D 64: 2 query tiles
+    // a piece); D > 64 has one buffer of K and V only, which cannot run ahead
+    p.stay = attn_dp(d.D) <= 64 && d.G() * p.qtiles <= 8 * p.dkv_splits;
     return p;
   }
   p.dkv_splits =
@@ -532,6 +535,23 @@ size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, int64_t Hk
     most = need > most ? need : most;
   }
   return most;
+}
+
+flare_status_t flare_attn_plan(int backward, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
+                               int64_t Nk, int64_t D, flare_dtype_t dt, int causal,
+                               int64_t* plan) {
+  if (plan == nullptr) return FLARE_ERR_INVALID_ARG;
+  FLARE_TRY(sizes(B, Hq, Hk, Nq, Nk, D, dt));
+  AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, causal);
+  d.q.sh = 1;   // every head has queries of its own
+  if (backward) {
+    const AttnBwdPlan p = attn_bwd_plan(d, dt, sm_count());
+    plan[0] = p.dkv_splits, plan[1] = p.dq_splits, plan[2] = p.stay;
+  } else {
+    const AttnPlan p = attn_plan(d, dt, sm_count());
+    plan[0] = p.qt, plan[1] = p.hpt, plan[2] = p.splits;
+  }
+  return FLARE_OK;
 }
 
 flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void* Y,

@@ -91,6 +91,7 @@ struct AttnBwdPlan {
   int tile = 0;
   int64_t ktiles = 0, dkv_units = 0, qtiles = 0, dq_units = 0;
   int dkv_splits = 1, dq_splits = 1;
+  bool stay = false;   // tensor cores: dK's and dV's CTAs take several pieces
 };
 
 AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms);

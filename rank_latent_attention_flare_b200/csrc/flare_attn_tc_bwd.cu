@@ -902,11 +902,9 @@ cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, AttnBwdArgs a, cudaSt
   if ((e = attn_map(&mk, a.K, d.k, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
   if ((e = attn_map(&mv, a.V, d.v, d.B, d.Hk, d.Nk, d.D, DP, 128, 1)) != cudaSuccess) return e;
   if ((e = attn_map(&mg, a.dY, d.dy, d.B, d.Hq, d.Nq, d.D, DP, 128, 1)) != cudaSuccess) return e;
-  // CTAs stay for several pieces of dK and dV where a piece is short (256
-  // latents over 65,536 tokens, D 64: 2 query tiles a piece)
+  static_assert((DkvLayout<DP>::KB == 2) == (DP <= 64), "attn_bwd_plan's rule");
   const int64_t pieces = a.dK ? p.dkv_units * p.dkv_splits : 0;
-  const bool stay = DkvLayout<DP>::KB == 2 && d.G() * p.qtiles <= 8 * p.dkv_splits;
-  a.dkv_ctas = (int)(stay ? imin64(pieces, sm_count()) : pieces);
+  a.dkv_ctas = (int)(p.stay ? imin64(pieces, sm_count()) : pieces);
   const int64_t grid = a.dkv_ctas + (a.dQ ? p.dq_units * p.dq_splits : 0);
   constexpr int kBytes =
       DkvLayout<DP>::BYTES > DqLayout<DP>::BYTES ? DkvLayout<DP>::BYTES : DqLayout<DP>::BYTES;
