@@ -594,11 +594,13 @@ FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void
  * 0; dY and Y are not read there.  y_low: NULL, or flare_attn_fwd's
  * y_low_save; with it sum_d dY Y is free of Y's rounding, which is otherwise
  * the larger part of the error of dQ and dK beyond their own roundings.
- * strides: NULL or 8 entries: Q, K, V, Y (and y_low), dY, dQ, dK, dV.  workspace: flare_attn_workspace_size(1, ...) bytes.
+ * strides: NULL or 8 entries: Q, K, V, Y (and y_low), dY, dQ, dK, dV.
+ * workspace: flare_attn_workspace_size(1, ...) bytes.
  */
 FLARE_API flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
-                                        const void* y_low, const void* dY, const float* lse, void* dQ, void* dK,
-                                        void* dV, const flare_strides_t* strides,
+                                        const void* y_low, const void* dY, const float* lse,
+                                        void* dQ, void* dK, void* dV,
+                                        const flare_strides_t* strides,
                                         const int32_t* q_lens, const int32_t* k_lens, int64_t B,
                                         int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D,
                                         flare_dtype_t dtype, float scale, int causal,

@@ -239,8 +239,8 @@ def attn_bwd(q, k, v, y, dy, lse, scale: Optional[float] = None, *, causal: bool
                            dv if need_dkv else v)
         st = _lib.load().flare_attn_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), y.data_ptr(), _p(y_low), dy.data_ptr(),
-            lse.data_ptr(), _p(dq), _p(dk), _p(dv), strides, _p(q_lens), _p(k_lens), B, Hq, Hk, Nq, Nk, D, code, s,
-            1 if causal else 0, ws.data_ptr(), ws.numel(), _raw_stream(index))
+            lse.data_ptr(), _p(dq), _p(dk), _p(dv), strides, _p(q_lens), _p(k_lens), B, Hq, Hk, Nq,
+            Nk, D, code, s, 1 if causal else 0, ws.data_ptr(), ws.numel(), _raw_stream(index))
     if st:
         _lib.check(st, "flare_attn_bwd")
     return dq, dk, dv

@@ -137,7 +137,8 @@ AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
     for (int which = 0; which < 4; ++which) {
       int& at = which & 1 ? p.dkv_splits : p.dq_splits;
       const int64_t tiles = which & 1 ? d.G() * p.qtiles : p.ktiles;
-      const int64_t hi = imin64(tiles, imax64(1, 4LL * slots / (which & 1 ? p.dkv_units : p.dq_units)));
+      const int64_t units = which & 1 ? p.dkv_units : p.dq_units;
+      const int64_t hi = imin64(tiles, imax64(1, 4LL * slots / units));
       int64_t last = 0;
       for (int64_t s = 1; s <= hi; ++s) {
         const int64_t each = (tiles + s - 1) / s;
@@ -162,7 +163,7 @@ namespace {
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
-AttnWs attn_ws_fwd(const AttnDims& d, flare_dtype_t, const AttnPlan& p) {
+AttnWs attn_ws_fwd(const AttnDims& d, const AttnPlan& p) {
   AttnWs w;
   w.part_ml = 256;
   const size_t recs = p.splits > 1 ? (size_t)p.units * p.splits * p.rows : 0;
@@ -171,7 +172,7 @@ AttnWs attn_ws_fwd(const AttnDims& d, flare_dtype_t, const AttnPlan& p) {
   return w;
 }
 
-AttnWs attn_ws_bwd(const AttnDims& d, flare_dtype_t, const AttnBwdPlan& p) {
+AttnWs attn_ws_bwd(const AttnDims& d, const AttnBwdPlan& p) {
   AttnWs w;
   const size_t dp = attn_dp(d.D);
   w.stats = 256;
@@ -511,7 +512,9 @@ AttnDims dims(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t
 
 // Zero strides (broadcast, or a dimension of one entry) -> one entry in the
 // tensor map, coordinate 0.
-int bcast_bits(const Tok& t, int k) { return (t.sb == 0 ? 1 << k : 0) | (t.sh == 0 ? 8 << k : 0); }
+int bcast_bits(const Tok& t, int k) {
+  return (t.sb == 0 ? 1 << k : 0) | (t.sh == 0 ? 8 << k : 0);
+}
 
 }  // namespace
 }  // namespace flare
@@ -530,8 +533,8 @@ size_t flare_attn_workspace_size(int backward, int64_t B, int64_t Hq, int64_t Hk
   for (int k = 0; k < 4; ++k) {
     AttnDims d = dims(B, Hq, Hk, Nq, Nk, D, k & 1);
     d.q.sh = k >> 1;
-    const size_t need = backward ? attn_ws_bwd(d, dt, attn_bwd_plan(d, dt, sms)).total
-                                 : attn_ws_fwd(d, dt, attn_plan(d, dt, sms)).total;
+    const size_t need = backward ? attn_ws_bwd(d, attn_bwd_plan(d, dt, sms)).total
+                                 : attn_ws_fwd(d, attn_plan(d, dt, sms)).total;
     most = need > most ? need : most;
   }
   return most;
@@ -573,10 +576,8 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   FLARE_TRY(check_tok(strides ? strides + 1 : nullptr, B, Hk, Nk, D, dt, false, &d.k));
   FLARE_TRY(check_tok(strides ? strides + 2 : nullptr, B, Hk, Nk, D, dt, false, &d.v));
   FLARE_TRY(check_tok(strides ? strides + 3 : nullptr, B, Hq, Nq, D, dt, true, &d.y));
-  d.q_lens = q_lens;
-  d.k_lens = k_lens;
   const AttnPlan p = attn_plan(d, dt, sm_count());
-  const AttnWs w = attn_ws_fwd(d, dt, p);
+  const AttnWs w = attn_ws_fwd(d, p);
   FLARE_TRY(check_workspace(workspace, workspace_bytes, w.total));
   if (p.units * p.splits > 0x7fffffffLL || B * Hq * Nq > 0x7fffffffLL * 4)
     return FLARE_ERR_UNSUPPORTED;   // grid.x
@@ -584,7 +585,8 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   char* ws = (char*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   AttnFwdArgs a = {};
-  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk), a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk);
+  a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
   a.hpt = p.hpt, a.qblocks = (int)p.qblocks, a.splits = p.splits, a.causal = d.causal;
   a.c = scale * kLog2e;
   a.q_lens = q_lens, a.k_lens = k_lens;
@@ -597,17 +599,18 @@ flare_status_t flare_attn_fwd(const void* Q, const void* K, const void* V, void*
   a.err = (uint32_t*)ws;
   a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2);
   FLARE_CUDA(attn_tc(dt) ? launch_attn_fwd_tc(Q, K, V, d, p, a, st)
-                         : launch_attn_fwd_simt(Q, K, V, d, p, a, st));
+                         : launch_attn_fwd_simt(Q, K, V, p, a, st));
   if (p.splits > 1) FLARE_CUDA(launch_attn_join(p, a, attn_dp(D), dt, st));
   return FLARE_OK;
 }
 
 flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const void* Y,
-                              const void* y_low, const void* dY, const float* lse, void* dQ, void* dK, void* dV,
-                              const flare_strides_t* strides, const int32_t* q_lens,
-                              const int32_t* k_lens, int64_t B, int64_t Hq, int64_t Hk, int64_t Nq,
-                              int64_t Nk, int64_t D, flare_dtype_t dt, float scale, int causal,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              const void* y_low, const void* dY, const float* lse, void* dQ,
+                              void* dK, void* dV, const flare_strides_t* strides,
+                              const int32_t* q_lens, const int32_t* k_lens, int64_t B, int64_t Hq,
+                              int64_t Hk, int64_t Nq, int64_t Nk, int64_t D, flare_dtype_t dt,
+                              float scale, int causal, void* workspace, size_t workspace_bytes,
+                              void* stream) {
   FLARE_TRY(sizes(B, Hq, Hk, Nq, Nk, D, dt));
   if (!std::isfinite(scale) || !(scale > 0.f)) return FLARE_ERR_INVALID_ARG;
   // dQ, or dK and dV together, may be left out
@@ -623,13 +626,11 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   for (int i = 0; i < 8; ++i) {
     const bool keys = i == 1 || i == 2 || i == 6 || i == 7;
     if ((i == 5 && !dQ) || (i > 5 && !dK)) continue;
-    FLARE_TRY(check_tok(strides ? strides + i : nullptr, B, keys ? Hk : Hq, keys ? Nk : Nq, D, dt, i >= 5,
-                 where[i]));
+    FLARE_TRY(check_tok(strides ? strides + i : nullptr, B, keys ? Hk : Hq, keys ? Nk : Nq, D, dt,
+                        i >= 5, where[i]));
   }
-  d.q_lens = q_lens;
-  d.k_lens = k_lens;
   const AttnBwdPlan p = attn_bwd_plan(d, dt, sm_count());
-  const AttnWs w = attn_ws_bwd(d, dt, p);
+  const AttnWs w = attn_ws_bwd(d, p);
   FLARE_TRY(check_workspace(workspace, workspace_bytes, w.total));
   const int64_t most = 0x7fffffffLL;
   if (p.dkv_units * p.dkv_splits + p.dq_units * p.dq_splits > most ||
@@ -639,7 +640,8 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   char* ws = (char*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   AttnBwdArgs a = {};
-  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk), a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
+  a.B = (int)B, a.Hq = (int)Hq, a.Hk = (int)Hk, a.G = (int)(Hq / Hk);
+  a.Nq = (int)Nq, a.Nk = (int)Nk, a.D = (int)D;
   a.tile = p.tile, a.ktiles = (int)p.ktiles, a.qtiles = (int)p.qtiles;
   a.dkv_splits = p.dkv_splits, a.dq_splits = p.dq_splits, a.causal = d.causal;
   a.dkv_units = p.dkv_units, a.dq_units = p.dq_units;
@@ -657,7 +659,7 @@ flare_status_t flare_attn_bwd(const void* Q, const void* K, const void* V, const
   a.bcast = bcast_bits(d.q, 0) | bcast_bits(d.k, 1) | bcast_bits(d.v, 2) |
             (d.dy.sb == 0 ? 64 : 0) | (d.dy.sh == 0 ? 128 : 0);
   FLARE_CUDA(launch_attn_bwd_prep(a, dt, st));
-  FLARE_CUDA(attn_tc(dt) ? launch_attn_bwd_tc(d, p, a, st) : launch_attn_bwd_simt(d, p, a, st));
+  FLARE_CUDA(attn_tc(dt) ? launch_attn_bwd_tc(d, p, a, st) : launch_attn_bwd_simt(p, a, st));
   if (dK && p.dkv_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 1, st));
   if (dQ && p.dq_splits > 1) FLARE_CUDA(launch_attn_bwd_sum(a, attn_dp(D), dt, 0, st));
   return FLARE_OK;

@@ -16,8 +16,6 @@ struct AttnDims {
   int64_t B = 0, Hq = 0, Hk = 0, Nq = 0, Nk = 0, D = 0;
   bool causal = false;
   Tok q, k, v, y, dy, dq, dk, dv;   // inputs may have zero batch / head strides (broadcast)
-  const int32_t* q_lens = nullptr;
-  const int32_t* k_lens = nullptr;
   int64_t G() const { return Hq / Hk; }
 };
 
@@ -25,7 +23,8 @@ struct AttnDims {
 struct AttnSeq {
   int ql, kl, off;   // valid queries, valid keys; causal: key j <= query i + off
   bool causal;
-  __device__ __forceinline__ AttnSeq(int Nq, int Nk) : ql(Nq), kl(Nk), off(Nk - Nq), causal(false) {}
+  __device__ __forceinline__ AttnSeq(int Nq, int Nk)
+      : ql(Nq), kl(Nk), off(Nk - Nq), causal(false) {}
   __device__ __forceinline__ AttnSeq(const int32_t* q_lens, const int32_t* k_lens, int b, int Nq,
                                      int Nk, bool causal_)
       : ql(Nq), kl(Nk), causal(causal_) {
@@ -104,8 +103,8 @@ struct AttnWs {
   size_t dq_part = 0, dkv_part = 0;            // backward: partial sums of the splits
   size_t total = 0;
 };
-AttnWs attn_ws_fwd(const AttnDims& d, flare_dtype_t dt, const AttnPlan& p);
-AttnWs attn_ws_bwd(const AttnDims& d, flare_dtype_t dt, const AttnBwdPlan& p);
+AttnWs attn_ws_fwd(const AttnDims& d, const AttnPlan& p);
+AttnWs attn_ws_bwd(const AttnDims& d, const AttnBwdPlan& p);
 
 // Zeroes the error word and reports lengths outside their range.  Called by
 // thread 0..31 of the first CTA of the first kernel of a call: a bounded wait
@@ -134,7 +133,8 @@ struct AttnFwdArgs {
   float2* part_ml;         // [units * splits][rows] (reference, sum), log2 units
   float* part_o;           // [units * splits][rows][DP]
   uint32_t* err;
-  int bcast;               // bits 0..5: q, k, v have one batch (1, 2, 4) or head (8, 16, 32) in memory
+  // bits 0..5: q, k, v have one batch (1, 2, 4) or head (8, 16, 32) in memory
+  int bcast;
 };
 
 struct AttnBwdArgs {
@@ -156,8 +156,8 @@ struct AttnBwdArgs {
 
 cudaError_t launch_attn_fwd_tc(const void* Q, const void* K, const void* V, const AttnDims& d,
                                const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st);
-cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnDims& d,
-                                 const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st);
+cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnPlan& p,
+                                 const AttnFwdArgs& a, cudaStream_t st);
 // Joins the records of the splits into Y and lse.
 cudaError_t launch_attn_join(const AttnPlan& p, const AttnFwdArgs& a, int dp, flare_dtype_t dt,
                              cudaStream_t st);
@@ -166,8 +166,7 @@ cudaError_t launch_attn_bwd_prep(const AttnBwdArgs& a, flare_dtype_t dt, cudaStr
 // The products; dQ, or dK and dV, may be NULL (not wanted).
 cudaError_t launch_attn_bwd_tc(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
                                cudaStream_t st);
-cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
-                                 cudaStream_t st);
+cudaError_t launch_attn_bwd_simt(const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st);
 // Sums the partials of the splits, in order, into dQ (which = 0) or dK and dV (1).
 cudaError_t launch_attn_bwd_sum(const AttnBwdArgs& a, int dp, flare_dtype_t dt, int which,
                                 cudaStream_t st);

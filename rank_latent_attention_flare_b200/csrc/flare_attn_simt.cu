@@ -104,8 +104,8 @@ __device__ __forceinline__ void prod_nn(const float* P, const float* B, int ty, 
 
 // Writes a thread's rows times f as rows [row0, n) of a token tensor.
 template <int DP>
-__device__ __forceinline__ void put_rows(float* p, int64_t sn, int row0, int n, int D, int ty, int tx,
-                                         const float (&c)[kR][DP / 16], float f) {
+__device__ __forceinline__ void put_rows(float* p, int64_t sn, int row0, int n, int D, int ty,
+                                         int tx, const float (&c)[kR][DP / 16], float f) {
   using C = Cols<DP>;
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -152,8 +152,8 @@ constexpr int kPFloats = kT * kPS;
 // a row are held by the 16 threads that share it.  P overwrites the key tile.
 template <int DP>
 __global__ void __launch_bounds__(kNT)
-    attn_fwd_simt_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V,
-                         const __grid_constant__ AttnFwdArgs A) {
+    attn_fwd_simt_kernel(const float* __restrict__ Q, const float* __restrict__ K,
+                         const float* __restrict__ V, const __grid_constant__ AttnFwdArgs A) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ float sm[];
@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(kNT) attn_dkv_simt_kernel(const __grid_constan
     put_part<DP>(p + kT * DP, ty, tx, dv);
     return;
   }
-  put_rows<DP>((float*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk, A.scale);
+  put_rows<DP>((float*)A.dK + b * A.dk.sb + hk * A.dk.sh, A.dk.sn, k0, A.Nk, A.D, ty, tx, dk,
+               A.scale);
   put_rows<DP>((float*)A.dV + b * A.dv.sb + hk * A.dv.sh, A.dv.sn, k0, A.Nk, A.D, ty, tx, dv, 1.f);
 }
 
@@ -421,7 +422,8 @@ __global__ void __launch_bounds__(kNT) attn_dq_simt_kernel(const __grid_constant
                  tx, dq);
     return;
   }
-  put_rows<DP>((float*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq, A.scale);
+  put_rows<DP>((float*)A.dQ + b * A.dq.sb + h * A.dq.sh, A.dq.sn, q0, A.Nq, A.D, ty, tx, dq,
+               A.scale);
 }
 
 template <typename... KA, typename... As>
@@ -452,18 +454,17 @@ cudaError_t bwd_t(const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnDims& d,
-                                 const AttnPlan& p, const AttnFwdArgs& a, cudaStream_t st) {
-  switch (attn_dp(d.D)) {
+cudaError_t launch_attn_fwd_simt(const void* Q, const void* K, const void* V, const AttnPlan& p,
+                                 const AttnFwdArgs& a, cudaStream_t st) {
+  switch (attn_dp(a.D)) {
     case 32: return fwd_t<32>(Q, K, V, p, a, st);
     case 64: return fwd_t<64>(Q, K, V, p, a, st);
     default: return fwd_t<128>(Q, K, V, p, a, st);
   }
 }
 
-cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnBwdPlan& p, const AttnBwdArgs& a,
-                                 cudaStream_t st) {
-  switch (attn_dp(d.D)) {
+cudaError_t launch_attn_bwd_simt(const AttnBwdPlan& p, const AttnBwdArgs& a, cudaStream_t st) {
+  switch (attn_dp(a.D)) {
     case 32: return bwd_t<32>(p, a, st);
     case 64: return bwd_t<64>(p, a, st);
     default: return bwd_t<128>(p, a, st);

@@ -15,12 +15,6 @@ namespace attn {
 
 using namespace tc;
 
-constexpr int kThreads = 384;        // warps 0-7 compute, 8 TMA, 9 MMA, 10 helper
-constexpr int kWarpTma = 8;
-constexpr int kWarpMma = 9;
-constexpr int kWarpAux = 10;
-constexpr int kRegsCompute = 216;    // 2 x 128 x 216 + 128 x 72 <= 384 x 168
-constexpr int kRegsProducer = 72;
 constexpr int kMinSmemBytes = 120 * 1024;   // keeps one CTA (and its TMEM) per SM
 
 // A tile of 128 rows of DP bf16 elements in shared memory: rows of 128 bytes
@@ -183,7 +177,8 @@ __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* p, const uint32_t (
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      v[k] = pack_bf16(__uint_as_float(o[8 * g + 2 * k]) * f, __uint_as_float(o[8 * g + 2 * k + 1]) * f);
+      v[k] = pack_bf16(__uint_as_float(o[8 * g + 2 * k]) * f,
+                       __uint_as_float(o[8 * g + 2 * k + 1]) * f);
     *reinterpret_cast<uint4*>(p + 8 * g) = make_uint4(v[0], v[1], v[2], v[3]);
     if (low == nullptr) continue;
 #pragma unroll

@@ -56,7 +56,8 @@ __device__ __forceinline__ void exp_cols(uint32_t (&a)[kCols], float c, float n,
 #pragma unroll
   for (int i = 0; i < kCols; i += 2) {
     const uint64_t x = fma_f32x2(f32x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), c2,
-                                 COLS ? f32x2(cols[COLS ? i : 0], cols[COLS ? i + 1 : 0]) : f32x2(n, n));
+                                 COLS ? f32x2(cols[COLS ? i : 0], cols[COLS ? i + 1 : 0])
+                                      : f32x2(n, n));
     float p0, p1;
     if (POLY > 0 && (i / 2) % (POLY > 0 ? POLY : 1) == POLY - 1) {
       exp2_fma_pair(x, p0, p1);
@@ -128,7 +129,8 @@ __device__ __forceinline__ void put_row(uint32_t taddr, int first, int step, boo
       if (rec) {
 #pragma unroll
         for (int x = 0; x < 32; x += 4)
-          *reinterpret_cast<uint4*>(rec + 32 * k + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          *reinterpret_cast<uint4*>(rec + 32 * k + x) =
+              make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
       } else if (32 * k < D) {
         store_bf16x32(out + 32 * k, o, f, 32 * k, D);
       }
@@ -490,15 +492,17 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& tmQ, const CUtensorM
           for (int v = 0; v < 2; ++v) {
             const Tok& to = v ? A.dv : A.dk;
             __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + w.b * to.sb + w.hk * to.sh;
-            float* rec = A.dkv_part + ((((int64_t)w.bh * A.ktiles + w.kt) * A.dkv_splits + w.split) * 2 + v) *
-                                          kAttnTile * DP;
+            const int64_t part = ((int64_t)w.bh * A.ktiles + w.kt) * A.dkv_splits + w.split;
+            float* rec = A.dkv_part + (part * 2 + v) * kAttnTile * DP;
             if (A.dkv_splits > 1) {
-              for (int x = lane; x < kAttnTile * DP / 4; x += 32) reinterpret_cast<uint4*>(rec)[x] = zero;
+              for (int x = lane; x < kAttnTile * DP / 4; x += 32)
+                reinterpret_cast<uint4*>(rec)[x] = zero;
             } else {
               const int per_row = A.D / 8;
               for (int x = lane; x < rows * per_row; x += 32) {
                 const int row = x / per_row;
-                *reinterpret_cast<uint4*>(out + (w.k0 + row) * to.sn + (x - row * per_row) * 8) = zero;
+                *reinterpret_cast<uint4*>(out + (w.k0 + row) * to.sn + (x - row * per_row) * 8) =
+                    zero;
               }
             }
           }
@@ -609,9 +613,8 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& tmQ, const CUtensorM
       const Tok& to = v ? A.dv : A.dk;
       __nv_bfloat16* out = (__nv_bfloat16*)(v ? A.dV : A.dK) + it.b * to.sb + it.hk * to.sh;
       float* rec = nullptr;
-      if (A.dkv_splits > 1)
-        rec = A.dkv_part +
-              ((((int64_t)it.bh * A.ktiles + it.kt) * A.dkv_splits + it.split) * 2 + v) * kAttnTile * DP;
+      const int64_t part = ((int64_t)it.bh * A.ktiles + it.kt) * A.dkv_splits + it.split;
+      if (A.dkv_splits > 1) rec = A.dkv_part + (part * 2 + v) * kAttnTile * DP;
       const bool own = key >= it.k0 && key < it.sq.kl;
       put_row<DP>(tmem + lb + (v ? TV : TK), w & 1, 2, true, true, v ? 1.f : A.scale,
                   out + key * to.sn, rec ? rec + (int64_t)(key - it.k0) * DP : nullptr, own, A.D);
@@ -721,7 +724,8 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
         const int kb = (A.bcast & 2) ? 0 : b, kh = (A.bcast & 16) ? 0 : hk;
         const int vb = (A.bcast & 4) ? 0 : b, vh = (A.bcast & 32) ? 0 : hk;
         mbar_arrive_expect_tx(q_full, 2 * T::BYTES);
-        load_tile<DP>(smem + L::Q_OFF, &tmQ, q_full, q0, (A.bcast & 8) ? 0 : h, (A.bcast & 1) ? 0 : b);
+        load_tile<DP>(smem + L::Q_OFF, &tmQ, q_full, q0, (A.bcast & 8) ? 0 : h,
+                      (A.bcast & 1) ? 0 : b);
         load_tile<DP>(smem + L::G_OFF, &tmG, q_full, q0, (A.bcast & 128) ? 0 : h,
                       (A.bcast & 64) ? 0 : b);
         int last = -1;
@@ -869,7 +873,8 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
     __nv_bfloat16* out = (__nv_bfloat16*)A.dQ + b * A.dq.sb + h * A.dq.sh + i * A.dq.sn;
     float* rec = nullptr;
     if (A.dq_splits > 1)
-      rec = A.dq_part + (((bh * A.qtiles + qt) * A.dq_splits + split) * kAttnTile + r) * (int64_t)DP;
+      rec = A.dq_part +
+            (((bh * A.qtiles + qt) * A.dq_splits + split) * kAttnTile + r) * (int64_t)DP;
     put_row<DP>(tmem + lb + TQ, w, 4, n > 0, n > 0 && !gone, A.scale, out, rec, live, A.D);
   }
   __syncwarp();
@@ -884,8 +889,10 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
 // launches, 567 as one; 16/4 heads of 4096, D 128: 385 and 364).
 template <int KS>
 __global__ void __launch_bounds__(kBThreads, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmG,
                     const __grid_constant__ AttnBwdArgs A) {
   pdl_wait();
   pdl_trigger();
@@ -912,7 +919,8 @@ cudaError_t bwd_t(const AttnDims& d, const AttnBwdPlan& p, AttnBwdArgs a, cudaSt
   if ((e = cudaFuncSetAttribute(attn_bwd_kernel<KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kSmem)) != cudaSuccess)
     return e;
-  e = launch_pdl(attn_bwd_kernel<KS>, dim3((unsigned)grid), kBThreads, kSmem, st, mq, mk, mv, mg, a);
+  e = launch_pdl(attn_bwd_kernel<KS>, dim3((unsigned)grid), kBThreads, kSmem, st, mq, mk, mv, mg,
+                 a);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 

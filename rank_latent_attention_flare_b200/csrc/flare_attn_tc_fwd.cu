@@ -40,7 +40,13 @@ namespace flare {
 namespace attn {
 namespace {
 
-constexpr float kRescaleTau = 8.0f;   // log2 units
+constexpr int kThreads = 384;        // warps 0-7 compute, 8 TMA, 9 MMA, 10 helper
+constexpr int kWarpTma = 8;
+constexpr int kWarpMma = 9;
+constexpr int kWarpAux = 10;
+constexpr int kRegsCompute = 216;    // 2 x 128 x 216 + 128 x 72 <= 384 x 168
+constexpr int kRegsProducer = 72;
+constexpr float kRescaleTau = 8.0f;  // log2 units
 
 template <int DP, int QT>
 struct FwdLayout {
@@ -51,7 +57,7 @@ struct FwdLayout {
   static constexpr int BAR_OFF = KV_OFF + STAGES * T::BYTES;
   static constexpr int NBARS = 2 * STAGES + 1 + 2 + 2 + 2 + 2 + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int ML_OFF = MISC_OFF + 16;               // QT = 1: the second record's (ref, sum)
+  static constexpr int ML_OFF = MISC_OFF + 16;   // QT = 1: the second record's (ref, sum)
   static constexpr int BYTES = ML_OFF + 128 * 8;
   // QT = 1: the second warpgroup's O, column by column, over the drained K / V ring
   static_assert(STAGES * T::BYTES >= 128 * DP * 4, "exchange area");
@@ -75,8 +81,10 @@ __device__ __forceinline__ int item_v(int j) {
 
 template <int KS, int QT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnFwdArgs A) {
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ AttnFwdArgs A) {
   pdl_wait();
   pdl_trigger();
   constexpr int DP = attn_dp(16 * KS);
