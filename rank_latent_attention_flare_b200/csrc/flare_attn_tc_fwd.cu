@@ -19,14 +19,12 @@
 //
 // TMEM: S of warpgroup w at columns 128 w, O at 256 + DP w.  P replaces the
 // first half of S: its first 64 keys are handed to the tensor core while the
-// others are computed, and S of the next tile follows the product.  For
-// D <= 64 there is room for P at 384 + 64 w: S of the next tile is then computed as soon as the softmax has read S, so that the
-// softmax does not wait for the tensor core (D = 64, 16 heads of 4096
-// tokens, all pairs: 113 us instead of 123).  All MMAs are issued by one thread, in batches whose
-// length is a compile-time constant (KS steps over D): a product under a
-// run-time condition of its own reached the tensor core with wrong operands.
-// They run in the order of issue, so that S of the next tile may be issued
-// behind the product that reads P from the same columns.
+// others are computed.  All MMAs are issued by one thread, in batches whose
+// length is a compile-time constant (KS steps over D).  They run in the order of
+// issue, so that S of the next tile is issued behind the product that reads P
+// from the same columns.  (P in columns of its own, where D <= 64 leaves room,
+// lets S of the next tile start earlier, but takes one more barrier a tile: 2x8
+// heads of 6000, D 64, 230 us against 223; of 1024, causal, 13.2 against 13.5.)
 //
 // Bound: per tile and SM the tensor core needs 4 D clocks for each of the two
 // products and the MUFU 1024 clocks for the exponentials, so D = 128 is bound
@@ -91,7 +89,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = FwdLayout<DP, QT>;
   using T = Tile<DP>;
   constexpr int NS = L::STAGES;
-  constexpr bool APART = DP <= 64;   // P apart from S
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* bars = (uint64_t*)(smem + L::BAR_OFF);
@@ -99,10 +96,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_empty = bars + NS;
   uint64_t* q_full = bars + 2 * NS;
   uint64_t* s_full = q_full + 1;     // [w] S written by the MMA
-  uint64_t* p_ready = s_full + 2;    // [w] S read and P written by the softmax
+  uint64_t* p_ready = s_full + 2;    // [w] P written by the softmax
   uint64_t* pv_done = p_ready + 2;   // [w] O holds the tile
-  // [w] S read (P apart from S), or the first half of P written
-  uint64_t* early = pv_done + 2;
+  uint64_t* early = pv_done + 2;     // [w] the first half of P written
   uint64_t* drain = early + 2;
   uint32_t* tmem_slot = (uint32_t*)(smem + L::MISC_OFF);
   volatile int* abort_flag = (volatile int*)(smem + L::MISC_OFF + 4);
@@ -240,27 +236,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + 128 * w, dQ + qo + T::kstep(kk), dK + ko + T::kstep(kk), idS, kk > 0);
           mma_commit(&s_full[w]);
         };
-        const uint32_t P0 = tmem + (APART ? 384 : 0), PW = APART ? 64 : 128;
         // O += P V over the keys [64 half, 64 half + 64) of tile j
         auto issue_PV = [&](int w, int j, int half, bool first) {
           const uint32_t vo = (uint32_t)((item_v<QT>(j) % NS) * T::BYTES) >> 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int kk = 4 * half + k;
-            mma_ts(tmem + 256 + DP * w, P0 + PW * w + 8 * kk, dV + vo + kk * T::MN_STEP, idPV,
+            mma_ts(tmem + 256 + DP * w, tmem + 128 * w + 8 * kk, dV + vo + kk * T::MN_STEP, idPV,
                    (!first || kk > 0) ? 1u : 0u);
           }
         };
         // waits for P of warpgroup w (its j-th use of the barriers) and multiplies
         auto do_PV = [&](int w, int j, int use) -> bool {
-          if (!APART) {
-            if (!mbar_wait(&early[w], (uint32_t)(use & 1))) return false;
-            tc_fence_after();
-            issue_PV(w, j, 0, use == 0);
-          }
+          if (!mbar_wait(&early[w], (uint32_t)(use & 1))) return false;
+          tc_fence_after();
+          issue_PV(w, j, 0, use == 0);
           if (!mbar_wait(&p_ready[w], (uint32_t)(use & 1))) return false;
           tc_fence_after();
-          if (APART) issue_PV(w, j, 0, use == 0);
           issue_PV(w, j, 1, use == 0);
           mma_commit(&pv_done[w]);
           return true;
@@ -272,28 +264,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n1 > 0) issue_S(1, 0);
             mma_commit(&kv_empty[item_k<QT>(0) % NS]);
           }
-        }
-        if (APART && QT == 2) {
-          // the warpgroups run half a tile apart: S0, then the other's product,
-          // S1, then this one's product
-          auto next_S = [&](int w, int j) -> bool {
-            if (!full(item_k<QT>(j + 1)) || !mbar_wait(&early[w], (uint32_t)(j & 1))) return false;
-            tc_fence_after();
-            issue_S(w, j + 1);
-            return true;
-          };
-          for (int j = 0; ok && j <= n; ++j) {
-            if (j + 1 < n0 && !(ok = next_S(0, j))) break;
-            if (j > 0) {
-              if (j - 1 < n1 && !(ok = full(item_v<QT>(j - 1)) && do_PV(1, j - 1, j - 1))) break;
-              mma_commit(&kv_empty[item_v<QT>(j - 1) % NS]);
-            }
-            if (j + 1 < n1 && !(ok = next_S(1, j))) break;
-            if (j + 1 < n) mma_commit(&kv_empty[item_k<QT>(j + 1) % NS]);
-            if (j < n0 && !(ok = full(item_v<QT>(j)) && do_PV(0, j, j))) break;
-            if (*abort_flag) ok = false;
-          }
-        } else if (QT == 2) {
           for (int j = 0; ok && j < n; ++j) {
             ok = full(item_v<QT>(j)) && (j + 1 >= n || full(item_k<QT>(j + 1)));
             if (!ok) break;
@@ -315,11 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_S(j, j);
             mma_commit(&kv_empty[item_k<QT>(j) % NS]);
           }
-          // S of tile j + 2 once S of tile j is read (P apart) or behind its product
+          // S of tile j + 2 behind the product of tile j
           auto next_S = [&](int j) -> bool {
             if (j + 2 >= n) return true;
             if (!full(item_k<QT>(j + 2))) return false;
-            if (APART && !mbar_wait(&early[j & 1], (uint32_t)((j >> 1) & 1))) return false;
             tc_fence_after();
             issue_S(j & 1, j + 2);
             mma_commit(&kv_empty[item_k<QT>(j + 2) % NS]);
@@ -330,9 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&kv_empty[item_v<QT>(j) % NS]);
             return true;
           };
-          for (int j = 0; ok && j < n + APART; ++j) {
-            if (APART) ok = next_S(j) && (j == 0 || next_PV(j - 1));
-            else ok = next_PV(j) && next_S(j);
+          for (int j = 0; ok && j < n; ++j) {
+            ok = next_PV(j) && next_S(j);
             if (*abort_flag) ok = false;
           }
         }
@@ -353,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lb = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lb + 128 * w;
     const uint32_t tO = tmem + lb + 256 + DP * w;
-    const uint32_t tP = APART ? tmem + lb + 384 + 64 * w : tS;
     // the row's query and head
     int i, h;
     bool live;
@@ -376,8 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok &= mbar_wait(&s_full[w], (uint32_t)(j & 1));
       if (!warp_live) {   // no row of this warp is stored
         warp_arrive(&early[w]);
-        // not ahead of the other warps' P of the tile before
-        if (APART && j > 0) ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
         warp_arrive(&p_ready[w]);
         if (!(ok = warp_all(ok))) break;
         continue;
@@ -392,10 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld64(tS, a[0]);
       tmem_ld64(tS + 64, a[1]);
       tmem_wait_ld_dep128(a[0], a[1]);
-      if (APART) {
-        tc_fence_before();
-        warp_arrive(&early[w]);
-      }
       if (masked) {
         mask_cols(a[0], 0, cl, ch);
         mask_cols(a[1], 64, cl, ch);
@@ -405,11 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       max_fold64(a[1], m4);
       const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
       top = max3_nan(top, mx, mx);
-      if (APART && j > 0) {   // the last product has read P (and O may be rescaled)
-        ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
-        __syncwarp();
-        tc_fence_after();
-      }
       const bool move = (mx - mr) * A.c > kRescaleTau;   // not for NaN
       if (warp_any(move)) {
         const float nm = move ? mx : mr;
@@ -417,11 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         mr = nm;
         if (j > 0) {
-          if (!APART) {
-            ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
-            __syncwarp();
-            tc_fence_after();
-          }
+          ok &= mbar_wait(&pv_done[w], (uint32_t)((j - 1) & 1));
+          __syncwarp();
+          tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < DP / 32; ++k) {
             uint32_t o[32];
@@ -442,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k) {
           uint32_t pk[16];
           exp_pack_pairs<16, decltype(poly)::value>(a[k >> 1] + 32 * (k & 1), A.c, neg, pk, s4);
-          tmem_st16(tP + 16 * k, pk);
-          if (!APART && k == 1) {
+          tmem_st16(tS + 16 * k, pk);
+          if (k == 1) {
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&early[w]);
