@@ -547,7 +547,9 @@ FLARE_API flare_status_t flare_eval_exp2(const float* x, float* y, int64_t n, in
  * Q, Y [B,Hq,Nq,D]; K, V [B,Hk,Nk,D]; Hq a multiple of Hk (the query heads
  * of a key head are neighbours).  Float32 or bf16 throughout; sums and the
  * softmax in float32.  With FLARE_BF16 the probabilities are rounded to bf16
- * before their product with V (so are P and dS in the backward).
+ * before their product with V (so are P and dS in the backward), and a third of
+ * the exponentials, which also enter lse, is off by up to 7.5e-5.  Y (and
+ * y_low_save) must not overlap Q, K or V.
  *
  *   strides   NULL (contiguous) or 4 entries: Q, K, V, Y.  As for the *_ex
  *             calls, except that Q, K and V may have a batch or head stride
@@ -591,7 +593,7 @@ FLARE_API flare_status_t flare_attn_fwd(const void* Q, const void* K, const void
  *   dK = scale dS^T Q,
  * dK and dV summed over the query heads of a key head.  dQ, or dK and dV
  * together, may be NULL (not wanted).  Gradients of rows past the lengths are
- * 0; dY and Y are not read there.  y_low: NULL, or flare_attn_fwd's
+ * 0; dY and Y are never used there, whatever they hold.  y_low: NULL, or flare_attn_fwd's
  * y_low_save; with it sum_d dY Y is free of Y's rounding, which is otherwise
  * the larger part of the error of dQ and dK beyond their own roundings.
  * strides: NULL or 8 entries: Q, K, V, Y (and y_low), dY, dQ, dK, dV.

@@ -162,11 +162,14 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
 
     q [B,Hq,Nq,D]; k, v [B,Hk,Nk,D] with Hq a multiple of Hk (the query heads
     of a key head are neighbours); D a multiple of 8 up to 128.  All may be
-    any views with D contiguous, k, v and q also expanded over batch or heads;
-    y takes q's layout, or goes to ``out``.  ``q_lens``, ``k_lens`` (int32 [B] on the device):
+    any views with D contiguous and rows on 16-byte boundaries, k, v and q also
+    expanded over batch or heads; y takes q's layout, or goes to ``out``, which
+    must not overlap q, k or v.  ``q_lens``, ``k_lens`` (int32 [B] on the device):
     valid queries and keys; rows past them are never used and y is 0 there.
     ``causal``: query i sees keys j <= i + (keys - queries), counted with the
-    lengths.  A query that sees no key gives 0."""
+    lengths.  A query that sees no key gives 0; one that sees a logit of NaN or
+    +inf gives NaN.  A length out of range is clamped; device_status(workspace)
+    reports it to a caller who passes the workspace."""
     index, B, Hq, Hk, Nq, Nk, D = _attn_dims(q, k, v)
     code = _f._dtype_code(q)
     s = D ** -0.5 if scale is None else float(scale)
@@ -289,8 +292,9 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, eps: float =
     [N, R/2], or [B, N, R/2] for positions of their own per batch element
     (None: no rotation); R a multiple of 16 up to D, which is a multiple of 8
     up to 128.  Pairs are (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
-    q and k may be any views with D contiguous; the outputs take their layout,
-    or go to ``out`` = (qo, ko), which may be q and k themselves."""
+    q and k may be any views with D contiguous and rows on 16-byte boundaries;
+    the outputs take their layout, or go to ``out`` = (qo, ko), which may be q and
+    k themselves."""
     index, B, Hq, Hk, N, D, R, sb = _norm_args(q, k, wq, wk, cos, sin)
     code = _f._dtype_code(q)
     with _on(index, stream):
@@ -418,7 +422,10 @@ def attn(q, k, v, scale: Optional[float] = None, *, causal: bool = False,
          q_lens: Optional[torch.Tensor] = None,
          k_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Softmax attention with autograd (arguments as attn_fwd).  Gradients go
-    to q, k and v: a scale that needs one is refused."""
+    to q, k and v: a scale that needs one is refused.  Kept for the backward: q,
+    k, v, y, lse, and in bf16 what rounding y left over, one more tensor of y's
+    size, which takes the gradients' error from 0.0026 - 0.0028 to 0.0024;
+    attn_fwd(save=True) and attn_bwd do without it, and take a workspace."""
     _no_gradient("scale", scale)
     if not torch.is_grad_enabled():   # a Function would not know, and save for a backward
         return attn_fwd(q, k, v, scale, causal=causal, q_lens=q_lens, k_lens=k_lens)

@@ -14,7 +14,15 @@ namespace {
 // CTA's start and end, `join` for one more launch and `part` for writing and
 // reading back one part's sums.  Pieces of equal size run in waves.  With a
 // causal mask their sizes spread evenly up to `tiles`, longest first: the
-// places share the sum, and a piece at the end leaves some of them idle.
+// places share the sum, and a piece at the end leaves some of them idle, for
+// about kTail of the longest.
+//
+// kTail: with 0 the forward of 8/2 heads of 1024, D 64, would be cut in three (20.8
+// us against 13.5) and the backward of 32/8 heads of 2048, D 128, in two (144
+// against 125).  With 0.3 most of sixteen causal sizes keep their plan, the
+// backward of 32/8 heads of 2048, D 64, would stay whole (85 us against 96).
+constexpr double kTail = 0.15;
+
 int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double setup, double join,
                   double part, double* estimate = nullptr) {
   int best = 1;
@@ -25,7 +33,7 @@ int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double s
     double cost;
     if (causal) {
       const double sum = (double)units * (0.5 * (double)tiles + (double)s * setup) / slots;
-      cost = fmax(longest, sum + 0.15 * longest);
+      cost = fmax(longest, sum + kTail * longest);
     } else {
       cost = (double)((units * s + slots - 1) / slots) * longest;
     }
@@ -45,7 +53,7 @@ int choose_splits(int64_t units, int64_t tiles, int slots, bool causal, double s
 double bwd_end(double n1, double c1, double n2, double c2, double slots, bool causal) {
   if (causal) {   // pieces are half a tile row on average, the last ones short
     const double sum = 0.5 * (n1 * c1 + n2 * c2) / slots;
-    return fmax(fmax(c1, c2), sum + 0.15 * c2);
+    return fmax(fmax(c1, c2), sum + kTail * c2);
   }
   const double q = floor(n1 / slots), late = n1 - q * slots, early = slots - late;
   // `late` places are free at t1, the others at t0
@@ -83,12 +91,14 @@ AttnPlan attn_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
   // one or a few tokens see about all keys
   const bool triangle = d.causal && 2 * d.Nq > d.Nk;
   // One or two query tiles a CTA: two read each key tile once for both and run
-  // at 1.06 times the rate (16 heads of 4096: 129 against 137 us at D 128, 111
-  // against 119 at D 64); one leaves no half empty (2 x 16 heads of 333 queries
-  // over 5001 keys, D 64: 42 against 48 us).  Times in microseconds: a tile 2.0
-  // (two), 1.06 (one) or 8 (CUDA cores, two CTAs an SM), a CTA's start and end
-  // about 4, a part's rows x DP floats at an SM's share of the memory bandwidth
-  // (5500 written and read back in a microsecond).
+  // faster (16 heads of 4096, one against two: 109 and 104 us at D 32, 117 and 106
+  // at D 64, 131 and 125 at D 128); one leaves no half empty (2 x 16 heads of 333
+  // queries over 5001 keys, D 64: 40 us against 45; D 128: 42 against 53).  Times
+  // in microseconds: a tile 2.0 (two) or 1.06 (one), as rounds of whole CTAs show
+  // them at D 128 (1.95 and 1.02; D 64: 1.66 and 0.91), or 8 (CUDA cores, two CTAs
+  // an SM), a CTA's start and end about 4 (a call of one tile takes 6 to 8), a
+  // join 3, a part's rows x DP floats at an SM's share of the memory bandwidth
+  // (6551 GB/s over 148 SMs: 5500 written and read back in a microsecond).
   double best = 1e300;
   for (int qt = 1; qt <= (tc && rows > kAttnTile ? 2 : 1); ++qt) {
     AttnPlan c = p;
@@ -120,12 +130,14 @@ AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
   const int slots = tc ? sms : 2 * sms;
   const double setup = tc ? 2.0 : 0.5, join = tc ? 4.0 : 0.5;
   const bool triangle = d.causal && d.Nq <= 2 * d.Nk && d.Nk <= 2 * d.Nq;
-  const double part = p.tile * attn_dp(d.D) / (tc ? 8000.0 : 22000.0);   // as the forward's
+  // as the forward's, in tiles of dQ (1.0 us at D 64, 1.5 at D 128; CUDA cores 4)
+  const double part = p.tile * attn_dp(d.D) / (tc ? 8000.0 : 22000.0);
   if (tc) {
-    // In tiles of dQ, of which one of dK and dV costs 1.2; each number of parts
-    // in turn, and only those that leave a piece fewer tiles than the one before
-    // (choosing for each side alone: 32/8 heads of 2048, D 128, causal 145 us
-    // against 126; 4 heads of 1000, D 64: 27 against 18.5).
+    // In tiles of dQ, of which one of dK and dV costs 1.2 (four whole rounds of
+    // each: 1.3; with 1.1 or 1.3 five of sixty sizes are cut otherwise); each
+    // number of parts in turn, and only those that leave a piece fewer tiles than
+    // the one before (choosing for each side alone: 32/8 heads of 2048, D 128,
+    // causal 145 us against 126; 4 heads of 1000, D 64: 27 against 18.5).
     const auto cost = [&](int64_t s1, int64_t s2) {
       const double t1 = (double)((d.G() * p.qtiles + s1 - 1) / s1);
       const double t2 = (double)((p.ktiles + s2 - 1) / s2);
@@ -148,8 +160,13 @@ AttnBwdPlan attn_bwd_plan(const AttnDims& d, flare_dtype_t dt, int sms) {
         if (c < best - 1e-9) best = c, at = (int)s;
       }
     }
-    // where a piece is short (256 latents over 65,536 tokens, D 64: 2 query tiles
-    // a piece); D > 64 has one buffer of K and V only, which cannot run ahead
+    // Where a piece is short, a CTA that stays saves its start and end and loads
+    // the next piece's K and V ahead (2 x 8 heads, D 64, the whole backward by
+    // query tiles a piece, one CTA a piece against staying: 1 tile 375 and 265 us,
+    // 2 253 and 198, 4 190 and 165, 8 155 and 142).  The border is a cautious one:
+    // 16 tiles, 275 and 262, would still gain, and so would D 128 with its one
+    // buffer of K and V (8 tiles 240 and 228); lengths that leave some pieces
+    // empty, which staying CTAs cannot share out, were not timed there.
     p.stay = attn_dp(d.D) <= 64 && d.G() * p.qtiles <= 8 * p.dkv_splits;
     return p;
   }

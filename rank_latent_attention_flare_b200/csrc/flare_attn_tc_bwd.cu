@@ -19,8 +19,8 @@
 // lane:  S = Q K^T, dP = dY V^T, dS = P (dP - delta), dQ += dS K.  S has two
 // buffers, so that P_j+1 is computed while {dQ_j, dP_j+1} run.
 //
-// Every batch of MMAs has a compile-time length (KS steps over D), see the
-// forward.  The tensor core runs the MMAs of the issuing thread in order, so
+// Every batch of MMAs has a compile-time length (KS steps over D), as the
+// forward's.  The tensor core runs the MMAs of the issuing thread in order, so
 // S_j+1 may be issued behind the product that reads P_j from its columns.
 //
 // P in float32 enters dS; P and dS are rounded to bf16 for their products.
@@ -33,12 +33,14 @@ namespace flare {
 namespace attn {
 namespace {
 
-// Every k-th pair of exponentials on the FMA pipe (tiles without a mask).
+// Every k-th pair of exponentials on the FMA pipe (tiles without a mask; 16 heads of
+// 4096 at D 32 / 64 / 128: 236 / 251 / 376 us; second 244 / 258 / 382, fourth 238 /
+// 253 / 383, none 241 / 258 / 386).
 constexpr int kBwdPoly = 3;
 
 // 16 softmax warps: warpgroup w of four takes 32 of a tile's 128 columns, so
 // that four warps on each SM sub-partition hide each other's latencies (with
-// eight warps of 64 columns the causal training step took 562 us).
+// eight warps of 64 columns the causal training step took 562 us, then 547).
 constexpr int kBThreads = 640;
 constexpr int kBWarpTma = 16, kBWarpMma = 17, kBWarpAux = 18;
 constexpr int kCols = 32;
@@ -253,8 +255,8 @@ struct Cursor {
 // number of the query tile since the start, c that of the piece.  With two
 // buffers of K and V the products of a piece follow those of the one before
 // without a break, and its loads run ahead; the sums of a piece are stored
-// between the tiles.  Long pieces are better left to the hardware, one CTA
-// each: it hands them out as SMs become free.
+// between the tiles.  Long pieces are left to the hardware, one CTA each: it
+// hands them out as SMs become free (attn_bwd_plan has the times of both).
 template <int KS>
 __device__ __forceinline__ void attn_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                          const CUtensorMap& tmV, const CUtensorMap& tmG,
@@ -885,8 +887,9 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& tmQ, const CUtensorMa
 }
 
 // Both in one launch, so that dQ's CTAs fill the SMs that the last of dK's and
-// dV's leave idle (2 x 8 heads of 6000, D 64, 5.1 waves each: 607 us as two
-// launches, 567 as one; 16/4 heads of 4096, D 128: 385 and 364).
+// dV's leave idle (when it was made, the register split not yet: 2 x 8 heads of
+// 6000, D 64, 5.1 waves each, 607 us as two launches and 567 as one; 16/4 heads of
+// 4096, D 128, 385 and 364).
 template <int KS>
 __global__ void __launch_bounds__(kBThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,

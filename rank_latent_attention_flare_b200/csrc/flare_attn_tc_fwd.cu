@@ -19,17 +19,22 @@
 //
 // TMEM: S of warpgroup w at columns 128 w, O at 256 + DP w.  P replaces the
 // first half of S: its first 64 keys are handed to the tensor core while the
-// others are computed.  All MMAs are issued by one thread, in batches whose
-// length is a compile-time constant (KS steps over D).  They run in the order of
-// issue, so that S of the next tile is issued behind the product that reads P
-// from the same columns.  (P in columns of its own, where D <= 64 leaves room,
+// others are computed.  All MMAs are issued by one thread, in the order in which
+// they run, so that S of the next tile is issued behind the product that reads P
+// from the same columns.  They come in batches whose length is a compile-time
+// constant (KS steps over D): a first form with each MMA under a run-time
+// condition of its own ended in illegal addresses, for a reason that reading did
+// not show.  Whole batches under run-time conditions, as here, are in every form
+// that has run since.  (P in columns of its own, where D <= 64 leaves room,
 // lets S of the next tile start earlier, but takes one more barrier a tile: 2x8
 // heads of 6000, D 64, 230 us against 223; of 1024, causal, 13.2 against 13.5.)
 //
 // Bound: per tile and SM the tensor core needs 4 D clocks for each of the two
 // products and the MUFU 1024 clocks for the exponentials, so D = 128 is bound
 // by both about equally and smaller D by the exponentials; single-token
-// calls are bound by reading the keys and values once.
+// calls are bound by reading the keys and values once.  D is filled up with
+// zeros: to 32, 64 or 128 columns in memory, and in the products to KS steps of 16
+// (D 16 costs as much as 32, 40 to 56 as 64, 104 to 120 as 128).
 #include <type_traits>
 
 #include "flare_attn_tc.cuh"
@@ -61,8 +66,11 @@ struct FwdLayout {
   static_assert(STAGES * T::BYTES >= 128 * DP * 4, "exchange area");
 };
 
-// Every third pair of exponentials runs on the FMA pipe (2, 4 and none: 2 to
-// 7% slower at 4096 tokens).
+// Every third pair of exponentials runs on the FMA pipe, off by 7.5e-5 at most
+// (in P, and through the row's sum in lse; half a step of bf16 is 3.9e-3).  16
+// heads of 4096 at D 32 / 64 / 128: 104 / 106 / 122 us; every second pair 115 / 123
+// / 129, every fourth 105 / 107 / 122, every sixth 108 / 113 / 124, none 110 / 115
+// / 125.
 constexpr int kFwdPoly = 3;
 
 // Ring order of the key and value tiles: the order in which the MMAs use
